@@ -1,7 +1,7 @@
 """ctypes binding of libnvfp4moe.so (argument marshalling only).
 
 Every function here has the name of the C entry point it calls (see
-``include/nvfp4_moe.h``) and does nothing but check tensor placement, dtypes
+``include/nvfp4_moe.h``, ``include/mxfp4.h`` and ``include/moe_balance.h``) and does nothing but check tensor placement, dtypes
 and shapes, allocate outputs and workspace with torch, pass raw device
 pointers and torch's current CUDA stream, and turn a non-OK status into an
 exception.  All arithmetic of the layer runs in the library's CUDA kernels;
@@ -40,7 +40,7 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-_vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_vp, _i, _f, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 
 
 class MoeWeightsStruct(ctypes.Structure):
@@ -101,6 +101,20 @@ _declare("moe_nvfp4_down", _i, ctypes.POINTER(MoeWeightsStruct), _vp, _vp, _vp, 
          _vp, _sz, _vp)
 
 _declare("nvfp4_block_stats_compute", _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp)
+_declare("mxfp4_scale_bytes", _sz, _i, _i, _i)
+_declare("mxfp4_quantize", _i, _vp, _i, _i, _i, _ll, _vp, _i, _i, _vp, _vp, _vp)
+_declare("mxfp4_quantize_transposed", _i, _vp, _i, _i, _i, _ll, _i, _vp, _vp, _vp)
+_declare("mxfp4_dequantize", _i, _vp, _vp, _i, _i, _i, _i, _vp, _ll, _vp)
+_declare("mxfp4_matmul_workspace_size", _sz)
+_declare("mxfp4_matmul", _i, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp, _sz, _vp)
+_declare("mxfp4_linear_workspace_size", _sz, _i, _i)
+_declare("mxfp4_linear", _i, _vp, _i, _i, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _ll, _vp,
+         _sz, _vp)
+_declare("moe_balance_loss_workspace_size", _sz, _i, _i, _i)
+_declare("moe_balance_loss", _i, _vp, _i, _i, _i, _ll, _vp, _i, _i, _vp, _vp, _i, _f, _vp, _vp, _vp, _vp, _vp, _sz,
+         _vp)
+_declare("moe_balance_loss_backward", _i, _vp, _i, _i, _i, _ll, _i, _i, _vp, _vp, _i, _f, _vp, _vp, _vp, _vp, _ll,
+         _vp)
 _declare("nvfp4_test_e2m1", _i, _vp, _i, _vp, _vp, _vp)
 _declare("nvfp4_test_e2m1_sweep", _i, ctypes.c_uint32, ctypes.c_uint64, _vp, _vp, _vp)
 _declare("nvfp4_test_e4m3", _i, _vp, _i, _vp, _vp, _vp)
@@ -121,6 +135,9 @@ EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
            "moe_nvfp4_gemm_workspace_size", "moe_nvfp4_gate_up",
            "moe_nvfp4_down", "moe_reap_keep",
            "nvfp4_block_stats_compute",
+           "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_quantize_transposed", "mxfp4_dequantize",
+           "mxfp4_matmul_workspace_size", "mxfp4_matmul", "mxfp4_linear_workspace_size", "mxfp4_linear",
+           "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "nvfp4_test_e2m1", "nvfp4_test_e2m1_sweep", "nvfp4_test_e4m3", "nvfp4_test_sigmoid",
            "nvfp4_test_mma_peak", "nvfp4_test_wait_timeout", "nvfp4_test_block_scale_div",
            "nvfp4_test_router_splits")
@@ -594,6 +611,343 @@ def moe_nvfp4_down(W: MoeWeights, h_codes, h_scales, expert_offsets, expert_coun
     _check(lib.moe_nvfp4_down(ctypes.byref(st), _p(h_codes), _p(h_scales), _p(expert_offsets), _p(expert_counts),
                               rows, _p(h_gscale), _p(row_weight), _p(yb), _p(yf), _p(ws), ws.numel(), _stream()))
     return {"y": y, "workspace": ws}
+
+
+# ---------------------------------------------------------------------------
+# MXFP4 matrices (include/mxfp4.h)
+# ---------------------------------------------------------------------------
+
+#: Element types of unquantised matrices (MXFP4_DTYPE_*).
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _on:
+    """Makes a tensor's device the current one for a call and gives the
+    device's current stream; every tensor of the call must live there."""
+    __slots__ = ("device", "prev", "stream")
+
+    def __init__(self, device, **tensors):
+        self.device = device
+        for name, t in tensors.items():
+            if t is not None and t.device != device:
+                raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        self.prev = cur if cur != self.device.index else -1
+        if self.prev >= 0:
+            torch.cuda.set_device(self.device)
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            torch.cuda.set_device(self.prev)
+
+
+def _matrix(t, name: str, dtypes=_DTYPES) -> int:
+    """Row stride (elements) of a CUDA matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a matrix with at least one column, got shape {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride {tuple(t.stride())})")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows (stride {tuple(t.stride())})")
+    return t.stride(0)
+
+
+def _vector(t, dtype, name: str, n: int):
+    _cuda(t, dtype, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return t
+
+
+@dataclass
+class Mxfp4:
+    """A rows x cols matrix in MXFP4: packed codes [rows, 16 ceil(cols / 32)]
+    (u8) and E8M0 scales (u8), "tiled" (what the products take) or
+    "canonical" ([rows, ceil(cols / 32)])."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+    layout: str = "tiled"
+
+    def __post_init__(self):
+        _cuda(self.codes, torch.uint8, "codes")
+        _cuda(self.scales, torch.uint8, "scales")
+        if self.layout not in ("tiled", "canonical"):
+            raise ValueError(f"MXFP4 layout must be 'tiled' or 'canonical', got {self.layout!r}")
+        blocks = (self.cols + 31) // 32
+        if self.rows < 0 or self.cols < 1:
+            raise ValueError(f"no MXFP4 matrix has shape {self.rows} x {self.cols}")
+        if self.codes.numel() < self.rows * blocks * 16:
+            raise ValueError(f"codes hold {self.codes.numel()} bytes; a {self.rows} x {self.cols} matrix has "
+                             f"{self.rows * blocks * 16}")
+        need = (self.rows * blocks if self.layout == "canonical"
+                else (self.rows + 127) // 128 * ((blocks + 3) // 4) * 512)
+        if self.scales.numel() < need:
+            raise ValueError(f"scales hold {self.scales.numel()} bytes; a {self.rows} x {self.cols} matrix has {need} "
+                             f"({self.layout})")
+        if self.scales.device != self.codes.device:
+            raise ValueError(f"scales must be on {self.codes.device}, got {self.scales.device}")
+
+
+def _mx_empty(rows: int, cols: int, layout: str, device) -> Mxfp4:
+    blocks = (cols + 31) // 32
+    codes = torch.empty((rows, blocks * 16), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, blocks) if layout == "canonical"
+                         else (rows + 127) // 128 * ((blocks + 3) // 4) * 512, dtype=torch.uint8, device=device)
+    return Mxfp4(codes, scales, rows, cols, layout)
+
+
+def _mx_out(out, rows: int, cols: int, layout: str, device) -> Mxfp4:
+    if out is None:
+        return _mx_empty(rows, cols, layout, device)
+    if (out.rows, out.cols, out.layout) != (rows, cols, layout):
+        raise ValueError(f"out is {out.rows} x {out.cols} ({out.layout}); this call writes {rows} x {cols} ({layout})")
+    return out
+
+
+def mxfp4_quantize(x: torch.Tensor, layout: str = "tiled", perm: torch.Tensor | None = None,
+                   out: Mxfp4 | None = None) -> Mxfp4:
+    """x [rows, cols] (bf16, fp16 or fp32, any row stride; or a stack
+    [n, rows, cols], contiguous, as n * rows rows) -> MXFP4.  With ``perm``
+    (int32) row r of the result is x[perm[r]], zeros where perm[r] names no
+    row."""
+    if isinstance(x, torch.Tensor) and x.dim() == 3:
+        if not x.is_contiguous():
+            raise ValueError("a stack of matrices must be contiguous")
+        x = x.reshape(-1, x.shape[2])
+    stride = _matrix(x, "x")
+    rows, cols = x.shape
+    n = rows
+    if perm is not None:
+        n = _cuda(perm, torch.int32, "perm").numel()
+    q = _mx_out(out, n, cols, layout, x.device)
+    with _on(x.device, perm=perm, out=q.codes) as stream:
+        _check(lib.mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride,
+                                  None if perm is None or n == 0 else perm.data_ptr(), n, _LAYOUTS[layout],
+                                  q.codes.data_ptr(), q.scales.data_ptr(), stream) if n else 0)
+    return q
+
+
+def mxfp4_quantize_transposed(x: torch.Tensor, layout: str = "tiled", out: Mxfp4 | None = None) -> Mxfp4:
+    """x [rows, cols] -> the MXFP4 matrix of its transpose (cols x rows, the
+    blocks along x's columns): the operand of a product that sums over rows."""
+    stride = _matrix(x, "x")
+    rows, cols = x.shape
+    q = _mx_out(out, cols, rows, layout, x.device)
+    with _on(x.device, out=q.codes) as stream:
+        _check(lib.mxfp4_quantize_transposed(x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride, _LAYOUTS[layout],
+                                             q.codes.data_ptr(), q.scales.data_ptr(), stream))
+    return q
+
+
+def mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of an MXFP4 matrix, [rows, cols] (exact in bf16 and fp32)."""
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    stride = _matrix(out, "out")
+    if tuple(out.shape) != (q.rows, q.cols):
+        raise ValueError(f"out must be {q.rows} x {q.cols}, got {tuple(out.shape)}")
+    with _on(q.codes.device, out=out) as stream:
+        _check(lib.mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _LAYOUTS[q.layout], q.rows, q.cols,
+                                    _DTYPES[out.dtype], out.data_ptr(), stride, stream))
+    return out
+
+
+def _product_args(M: int, b: Mxfp4, out_dtype, out, bias, row_weight, expert_offsets, expert_counts):
+    """Checks a product's tensors; returns (E, N, out, its row stride)."""
+    if b.layout != "tiled":
+        raise ValueError("a product takes tiled scales; quantise with layout='tiled'")
+    E = 0
+    if expert_offsets is not None:
+        E = _cuda(expert_offsets, torch.int32, "expert_offsets").numel() - 1
+        if E < 1 or b.rows % E:
+            raise ValueError(f"expert_offsets of {E + 1} entries do not divide b's {b.rows} rows into experts")
+        if expert_counts is not None:
+            _vector(expert_counts, torch.int32, "expert_counts", E)
+    elif expert_counts is not None:
+        raise ValueError("expert_counts go with expert_offsets")
+    N = b.rows // max(E, 1)
+    if row_weight is not None:
+        _vector(row_weight, torch.float32, "row_weight", M)
+    if bias is not None:
+        _vector(bias, torch.float32, "bias", b.rows)
+    if out is None:
+        # grouped: the rows of no expert are not written
+        make = torch.zeros if E else torch.empty
+        out = make((M, N), dtype=out_dtype, device=b.codes.device)
+    stride = _matrix(out, "out")
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be {M} x {N}, got {tuple(out.shape)}")
+    return E, N, out, stride
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def mxfp4_matmul_workspace_size() -> int:
+    return lib.mxfp4_matmul_workspace_size()
+
+
+def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                 bias: torch.Tensor | None = None, row_weight: torch.Tensor | None = None,
+                 expert_offsets: torch.Tensor | None = None, expert_counts: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """a (M x K) times the transpose of b (N x K): y[m] = row_weight[m] *
+    (sum_k a[m, k] b[n, k] + bias[n]), [M, N].  With ``expert_offsets`` (int32
+    [E + 1], multiples of 128 as moe_route gives them) b holds E matrices of
+    N rows and rows [offsets[e], offsets[e] + counts[e]) meet matrix e; the
+    other rows of ``out`` are left as they were (0 in a new one)."""
+    if a.layout != "tiled":
+        raise ValueError("a product takes tiled scales; quantise with layout='tiled'")
+    if a.cols != b.cols:
+        raise ValueError(f"a has {a.cols} columns and b {b.cols}")
+    E, N, out, stride = _product_args(a.rows, b, out_dtype, out, bias, row_weight, expert_offsets, expert_counts)
+    if workspace is None:
+        workspace = _workspace(256, a.codes.device)
+    else:
+        _cuda(workspace, torch.uint8, "workspace")
+    with _on(a.codes.device, b=b.codes, out=out, bias=bias, row_weight=row_weight, expert_offsets=expert_offsets,
+             expert_counts=expert_counts, workspace=workspace) as stream:
+        _check(lib.mxfp4_matmul(a.codes.data_ptr(), a.scales.data_ptr(), a.rows, b.codes.data_ptr(),
+                                b.scales.data_ptr(), N, a.cols, E, _ptr(expert_offsets), _ptr(expert_counts),
+                                _ptr(row_weight), _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride,
+                                workspace.data_ptr(), workspace.numel(), stream))
+    return out
+
+
+def mxfp4_linear_workspace_size(M: int, K: int) -> int:
+    return lib.mxfp4_linear_workspace_size(M, K)
+
+
+def mxfp4_linear(x: torch.Tensor, w: Mxfp4, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                 bias: torch.Tensor | None = None, row_weight: torch.Tensor | None = None,
+                 perm: torch.Tensor | None = None, expert_offsets: torch.Tensor | None = None,
+                 expert_counts: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """mxfp4_matmul with a = x (or, with ``perm``, its rows x[perm[r]])
+    quantised in the call.  x is [rows, K], any row stride; the result has
+    x's dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    x_stride = _matrix(x, "x")
+    rows, K = x.shape
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns and w {w.cols}")
+    M = rows if perm is None else _cuda(perm, torch.int32, "perm").numel()
+    E, N, out, stride = _product_args(M, w, out_dtype or x.dtype, out, bias, row_weight, expert_offsets,
+                                      expert_counts)
+    if M == 0:
+        return out
+    if workspace is None:
+        workspace = _workspace(lib.mxfp4_linear_workspace_size(M, K), x.device)
+    else:
+        _cuda(workspace, torch.uint8, "workspace")
+    with _on(x.device, w=w.codes, out=out, bias=bias, row_weight=row_weight, perm=perm,
+             expert_offsets=expert_offsets, expert_counts=expert_counts, workspace=workspace) as stream:
+        _check(lib.mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], rows, x_stride, _ptr(perm), M, w.codes.data_ptr(),
+                                w.scales.data_ptr(), N, K, E, _ptr(expert_offsets), _ptr(expert_counts),
+                                _ptr(row_weight), _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride,
+                                workspace.data_ptr(), workspace.numel(), stream))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the router's balance loss (include/moe_balance.h)
+# ---------------------------------------------------------------------------
+
+BALANCE_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+@dataclass
+class BalanceLoss:
+    """Outputs of moe_balance_loss and what its backward needs of the call."""
+    loss: torch.Tensor               # f32 [1]
+    counts: torch.Tensor             # i32 [S, E] choices per expert
+    tokens: torch.Tensor             # i32 [S + 1] tokens per sequence, then the sequences that have any
+    probs: torch.Tensor              # f32 [S, E] mean shares
+    k: int
+    score: str
+    coeff: float
+    token_mask: torch.Tensor | None
+    seq_offsets: torch.Tensor | None
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, S: int = 1) -> int:
+    return lib.moe_balance_loss_workspace_size(T, E, S)
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float, score: str = "sigmoid",
+                     token_mask: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> BalanceLoss:
+    """Load-balance loss of a router from its logits [T, E] (fp32, bf16 or
+    fp16, any row stride) and choices topk_idx [T, k] (int32, as moe_route
+    gives them).  ``token_mask`` (bool or uint8 [T]): tokens to count.
+    ``seq_offsets`` (int32 [S + 1]): the loss per sequence, averaged over the
+    sequences that have tokens."""
+    stride = _matrix(logits, "logits")
+    T, E = logits.shape
+    _cuda(topk_idx, torch.int32, "topk_idx")
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k], got {tuple(topk_idx.shape)}")
+    k = topk_idx.shape[1]
+    if score not in BALANCE_SCORES:
+        raise ValueError(f"score must be one of {', '.join(BALANCE_SCORES)}, got {score!r}")
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _vector(token_mask, torch.uint8, "token_mask", T)
+    S = 1
+    if seq_offsets is not None:
+        S = _cuda(seq_offsets, torch.int32, "seq_offsets").numel() - 1
+    if S < 1:
+        raise ValueError("seq_offsets must hold at least two values")
+    dev = logits.device
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty(S + 1, dtype=torch.int32, device=dev)
+    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _workspace(lib.moe_balance_loss_workspace_size(T, E, S), dev)
+    else:
+        _cuda(workspace, torch.uint8, "workspace")
+    with _on(dev, topk_idx=topk_idx, token_mask=token_mask, seq_offsets=seq_offsets, workspace=workspace) as stream:
+        _check(lib.moe_balance_loss(logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, topk_idx.data_ptr(), k,
+                                    BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff,
+                                    loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel(), stream))
+    return BalanceLoss(loss, counts, tokens, probs, k, score, coeff, token_mask, seq_offsets)
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss: torch.Tensor,
+                              out: torch.Tensor | None = None) -> torch.Tensor:
+    """grad_loss (f32 [1] on the device) times the gradient of fwd.loss with
+    respect to logits, in logits' dtype; ``fwd`` is the forward call's result
+    for the same logits."""
+    stride = _matrix(logits, "logits")
+    T, E = logits.shape
+    if fwd.counts.shape[1] != E:
+        raise ValueError(f"logits have {E} experts and the forward call had {fwd.counts.shape[1]}")
+    if fwd.token_mask is not None and fwd.token_mask.numel() != T:
+        raise ValueError(f"logits have {T} tokens and the forward call's mask {fwd.token_mask.numel()}")
+    _vector(grad_loss, torch.float32, "grad_loss", 1)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    out_stride = _matrix(out, "out", (logits.dtype,))
+    if tuple(out.shape) != (T, E):
+        raise ValueError(f"out must be {T} x {E}, got {tuple(out.shape)}")
+    with _on(logits.device, counts=fwd.counts, grad_loss=grad_loss, out=out) as stream:
+        _check(lib.moe_balance_loss_backward(logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, fwd.k,
+                                             BALANCE_SCORES[fwd.score], _ptr(fwd.token_mask), _ptr(fwd.seq_offsets),
+                                             fwd.counts.shape[0], fwd.coeff, fwd.counts.data_ptr(),
+                                             fwd.tokens.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), out_stride,
+                                             stream))
+    return out
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,530 @@
+// Load-balance loss of the router, per-expert counts, and the gradient.
+//
+// Forward, two kernels.  balance_pieces_kernel streams the logits once: a
+// group of lanes holds one token's row, takes its softmax (or sigmoid shares)
+// in registers and adds it to per-lane sums; a block covers a fixed chunk of
+// tokens and leaves, for every (chunk, sequence) piece it meets, the piece's
+// probability sums, counts and tokens.  Pieces are numbered chunk + sequence:
+// going along the tokens either the chunk or the sequence advances, so the
+// numbers are distinct, and chunks + S entries hold them for any lengths.
+// balance_finish_kernel adds each sequence's pieces in order; its last block
+// adds the sequences.  Every sum has a fixed order.
+//
+// Backward, one kernel: the same row arithmetic, with the experts' shares f
+// of the row's sequence held in registers while the sequence lasts.
+//
+// Bound: HBM (logits in; gradient out), with one exponential (softmax) or one
+// exponential and one reciprocal (sigmoid) per element close behind.
+#include <algorithm>
+
+#include "mx.cuh"
+#include "../../include/moe_balance.h"
+
+namespace nvfp4moe {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalMaxE = 1024;
+constexpr int kBalMaxK = 32;
+
+struct BalanceShape {
+  int T, E, S, k, score;
+  int lanes;                  // lanes per row, a power of two
+  long long stride;           // logits row stride, elements
+  const int32_t* seq_offsets; // null: one sequence
+  const uint8_t* mask;        // null: every token
+};
+
+NVDEV int seq_begin(const BalanceShape& b, int s) {
+  return b.seq_offsets ? min(max(__ldg(b.seq_offsets + s), 0), b.T) : (s > 0 ? b.T : 0);
+}
+// The last sequence that starts at or before token t, or -1.
+NVDEV int seq_of(const BalanceShape& b, int t) {
+  int lo = -1, hi = b.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seq_begin(b, mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Four neighbouring logits from element e of a row; -inf past E.
+template <typename T, bool VEC>
+NVDEV void load4(const void* logits, long long row, int e, int E, bool live, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = -INFINITY;
+  if (!live || e >= E) return;
+  if constexpr (VEC) {
+    if constexpr (T::size == 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e));
+      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + row + e));
+      v[0] = T::lo(u.x); v[1] = T::hi(u.x); v[2] = T::lo(u.y); v[3] = T::hi(u.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i < E) {
+        if constexpr (T::size == 4) v[i] = __ldg(static_cast<const float*>(logits) + row + e + i);
+        else v[i] = T::from(__ldg(static_cast<const uint16_t*>(logits) + row + e + i));
+      }
+  }
+}
+
+template <int N>
+NVDEV float row_max(const float* v, int lanes) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+template <int N>
+NVDEV float row_sum(const float* v, int lanes) {
+  float z = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) z += v[i];
+  for (int o = lanes >> 1; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return z;
+}
+
+// l -> shares p (in place) and, where asked, d = dlog(score)/dl (1 for
+// softmax, sigma(-l) for sigmoid).  Sigmoid: while the row's largest logit is
+// above -60 the sigmas are taken as they are (one that underflows is below
+// 1e-12 of the largest); below it sigma(l) is exp(l) to the last bit of fp32,
+// and the shares are a softmax, which nothing underflows.  1 - sigma is taken
+// as t sigma with t = exp(-l) for l >= 0, where 1 - sigma would cancel.
+template <int N, bool GRAD>
+NVDEV void row_shares(float* l, float* d, int lanes, int score) {
+  const float m = row_max<N>(l, lanes);
+  const bool soft = score == MOE_BALANCE_SOFTMAX || m < -60.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float x = l[i];
+    const float t = expf(soft ? x - m : -x);
+    const float sg = __fdividef(1.0f, 1.0f + t);
+    if (GRAD) d[i] = soft ? 1.0f : (x < 0.0f ? 1.0f - sg : t * sg);
+    // -inf is a masked expert (m = -inf: all of them, x - m is NaN there)
+    l[i] = x == -INFINITY ? 0.0f : (soft ? t : sg);
+  }
+  const float z = row_sum<N>(l, lanes);
+  const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+#pragma unroll
+  for (int i = 0; i < N; ++i) l[i] *= inv;
+}
+
+struct BalancePieces {
+  float* probs;       // [pieces][E]
+  int32_t* counts;    // [pieces][E]
+  int32_t* tokens;    // [pieces]
+  uint32_t* status;   // [0] status word, [1] finished blocks
+};
+
+// V x 4 logits a lane; UR rows in flight per group of lanes.
+template <typename T, bool VEC, int V, int UR>
+__global__ void __launch_bounds__(kBalThreads) balance_pieces_kernel(const void* __restrict__ logits,
+                                                                     const int32_t* __restrict__ topk_idx,
+                                                                     const BalanceShape b, int chunk,
+                                                                     const BalancePieces out) {
+  extern __shared__ float s_sum[];                          // [warps][E], then int counts [E]
+  __shared__ int s_tokens;
+  int32_t* s_cnt = reinterpret_cast<int32_t*>(s_sum + kBalWarps * b.E);
+  griddep_wait();
+  griddep_launch();
+  if (blockIdx.x == 0 && threadIdx.x < 2) out.status[threadIdx.x] = 0u;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = b.lanes, l = lane & (L - 1), g = lane / L, G = 32 / L;
+  const int c0 = (int)min((long long)blockIdx.x * chunk, (long long)b.T);
+  const int c1 = (int)min((long long)c0 + chunk, (long long)b.T);
+  if (c0 >= c1) return;
+  for (int s = max(seq_of(b, c0), 0); s < b.S; ++s) {
+    const int s0 = seq_begin(b, s);
+    if (s0 >= c1) break;
+    const int r0 = max(c0, s0), r1 = min(c1, seq_begin(b, s + 1));
+    if (r0 >= r1) continue;
+    __syncthreads();                                        // the last piece has left shared memory
+    for (int e = threadIdx.x; e < b.E; e += kBalThreads) s_cnt[e] = 0;
+    if (threadIdx.x == 0) s_tokens = 0;
+    __syncthreads();
+    // the choices: integer atomics, whose order does not matter
+    const long long pairs = (long long)(r1 - r0) * b.k;
+    for (long long i = threadIdx.x; i < pairs; i += kBalThreads) {
+      const int t = r0 + (int)(i / b.k);
+      const int e = __ldg(topk_idx + (size_t)r0 * b.k + i);
+      if ((!b.mask || __ldg(b.mask + t)) && e >= 0 && e < b.E) atomicAdd(&s_cnt[e], 1);
+    }
+    int kept = 0;
+    float acc[V * 4];
+#pragma unroll
+    for (int i = 0; i < V * 4; ++i) acc[i] = 0.0f;
+    for (int base = r0 + warp * G; base < r1; base += kBalWarps * G * UR) {
+      float v[UR][V * 4];
+      bool live[UR];
+#pragma unroll
+      for (int u = 0; u < UR; ++u) {
+        const int t = base + u * kBalWarps * G + g;
+        live[u] = t < r1 && (!b.mask || __ldg(b.mask + t));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          load4<T, VEC>(logits, (long long)t * b.stride, (i * L + l) * 4, b.E, live[u], v[u] + 4 * i);
+      }
+#pragma unroll
+      for (int u = 0; u < UR; ++u) {
+        row_shares<V * 4, false>(v[u], nullptr, L, b.score);
+        if (live[u]) {
+          if (l == 0) ++kept;
+#pragma unroll
+          for (int i = 0; i < V * 4; ++i) acc[i] += v[u][i];
+        }
+      }
+    }
+    // lanes of the warp that hold the same experts, then the warps in order
+#pragma unroll
+    for (int i = 0; i < V * 4; ++i)
+      for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (g == 0) {
+#pragma unroll
+      for (int i = 0; i < V * 4; ++i) {
+        const int e = ((i >> 2) * L + l) * 4 + (i & 3);
+        if (e < b.E) s_sum[warp * b.E + e] = acc[i];
+      }
+    }
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if (lane == 0) atomicAdd(&s_tokens, kept);
+    __syncthreads();
+    const size_t piece = (size_t)blockIdx.x + s;
+    for (int e = threadIdx.x; e < b.E; e += kBalThreads) {
+      float z = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBalWarps; ++w) z += s_sum[w * b.E + e];
+      out.probs[piece * b.E + e] = z;
+      out.counts[piece * b.E + e] = s_cnt[e];
+    }
+    if (threadIdx.x == 0) out.tokens[piece] = s_tokens;
+  }
+}
+
+// One block per (sequence, 32 experts): warp w adds pieces w, w + 8, ..., the
+// warps' sums join in warp order, all in fp64.
+__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(const BalanceShape b, int chunk,
+                                                                     const BalancePieces in, double* __restrict__ dots,
+                                                                     float coeff, float* __restrict__ loss,
+                                                                     int32_t* __restrict__ counts,
+                                                                     int32_t* __restrict__ tokens,
+                                                                     float* __restrict__ probs) {
+  __shared__ double s_p[kBalWarps][32];
+  __shared__ int32_t s_c[kBalWarps][32];
+  __shared__ int s_n[kBalWarps];
+  __shared__ bool s_last;
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int eg = gridDim.y, s = blockIdx.x, e = blockIdx.y * 32 + lane;
+  const int r0 = seq_begin(b, s), r1 = seq_begin(b, s + 1);
+  double p = 0.0;
+  int c = 0, n = 0;
+  if (r0 < r1) {
+    const int first = r0 / chunk, last = (r1 - 1) / chunk;
+#pragma unroll 4
+    for (int i = first + warp; i <= last; i += kBalWarps) {
+      const size_t piece = (size_t)i + s;
+      if (e < b.E) {
+        p += (double)in.probs[piece * b.E + e];
+        c += in.counts[piece * b.E + e];
+      }
+      n += in.tokens[piece];                               // the same in every lane
+    }
+  }
+  s_p[warp][lane] = p;
+  s_c[warp][lane] = c;
+  if (lane == 0) s_n[warp] = n;
+  __syncthreads();
+  if (warp == 0) {
+    p = 0.0;
+    c = n = 0;
+#pragma unroll
+    for (int w = 0; w < kBalWarps; ++w) {
+      p += s_p[w][lane];
+      c += s_c[w][lane];
+      n += s_n[w];
+    }
+    const double mean = n > 0 ? p / n : 0.0;
+    double dot = n > 0 ? (double)c * b.E / ((double)b.k * n) * mean : 0.0;
+    if (e < b.E) {
+      counts[(size_t)s * b.E + e] = c;
+      probs[(size_t)s * b.E + e] = (float)mean;
+    }
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) {
+      dots[(size_t)s * eg + blockIdx.y] = dot;
+      if (blockIdx.y == 0) tokens[s] = n;
+      __threadfence();
+      s_last = atomicAdd(&in.status[1], 1u) == gridDim.x * gridDim.y - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // the last block to finish adds the sequences, in a fixed order
+  __threadfence();
+  double z = 0.0;
+  int full = 0;
+  for (long long i = threadIdx.x; i < (long long)b.S * eg; i += kBalThreads) z += __ldcg(dots + i);
+  for (int i = threadIdx.x; i < b.S; i += kBalThreads) full += __ldcg(tokens + i) > 0;
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  full = __reduce_add_sync(0xffffffffu, full);
+  __syncthreads();
+  if (lane == 0) {
+    s_p[warp][0] = z;
+    s_n[warp] = full;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    z = 0.0;
+    full = 0;
+    for (int w = 0; w < kBalWarps; ++w) {
+      z += s_p[w][0];
+      full += s_n[w];
+    }
+    *loss = full ? (float)((double)coeff / full * z) : 0.0f;
+    tokens[b.S] = full;
+  }
+}
+
+template <typename T, bool VEC, int V, int UR>
+__global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(const void* __restrict__ logits,
+                                                                       const BalanceShape b, int rows_per_warp,
+                                                                       float coeff, const int32_t* __restrict__ counts,
+                                                                       const int32_t* __restrict__ tokens,
+                                                                       const float* __restrict__ grad_loss,
+                                                                       void* __restrict__ dlogits,
+                                                                       long long grad_stride) {
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = b.lanes, l = lane & (L - 1), g = lane / L, G = 32 / L;
+  const long long w0 = ((long long)blockIdx.x * kBalWarps + warp) * rows_per_warp;
+  const int r1 = (int)min(w0 + rows_per_warp, (long long)b.T);
+  if (w0 >= b.T) return;
+  const float up = *grad_loss;
+  const int full = tokens[b.S];
+  // this group's sequence: the tokens [s0, s1) that its shares f hold for
+  int s0 = 0, s1 = 0;
+  float f[V * 4], scale = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V * 4; ++i) f[i] = 0.0f;
+  for (int base = (int)w0; base < r1; base += G * UR) {
+    float v[UR][V * 4];
+    bool live[UR];
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+      const int t = base + u * G + g;
+      live[u] = t < r1 && (!b.mask || __ldg(b.mask + t));
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        load4<T, VEC>(logits, (long long)t * b.stride, (i * L + l) * 4, b.E, live[u], v[u] + 4 * i);
+    }
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+      const int t = base + u * G + g;
+      if (live[u] && !(t >= s0 && t < s1)) {
+        const int s = seq_of(b, t);
+        scale = 0.0f;
+        s0 = s1 = 0;
+        if (s >= 0 && t < seq_begin(b, s + 1)) {
+          s0 = seq_begin(b, s);
+          s1 = seq_begin(b, s + 1);
+          const int n = __ldg(tokens + s);
+          const float fe = n > 0 ? (float)((double)b.E / ((double)b.k * n)) : 0.0f;
+          scale = n > 0 && full > 0 ? (float)((double)up * coeff / ((double)full * n)) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < V * 4; ++i) {
+            const int e = ((i >> 2) * L + l) * 4 + (i & 3);
+            f[i] = e < b.E ? (float)__ldg(counts + (size_t)s * b.E + e) * fe : 0.0f;
+          }
+        }
+      }
+      const bool in_seq = live[u] && t >= s0 && t < s1;
+      float d[V * 4], fp[V * 4];
+      row_shares<V * 4, true>(v[u], d, L, b.score);
+#pragma unroll
+      for (int i = 0; i < V * 4; ++i) fp[i] = f[i] * v[u][i];
+      const float dot = row_sum<V * 4>(fp, L);
+      if (t < r1) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = (i * L + l) * 4;
+          if (e >= b.E) continue;
+          float o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = in_seq ? scale * (v[u][4 * i + j] * (f[4 * i + j] - dot)) * d[4 * i + j] : 0.0f;
+          const long long at = (long long)t * grad_stride + e;
+          if constexpr (VEC) {
+            if constexpr (T::size == 4)
+              *reinterpret_cast<float4*>(static_cast<float*>(dlogits) + at) = make_float4(o[0], o[1], o[2], o[3]);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dlogits) + at) =
+                  make_uint2(T::pack(o[0], o[1]), T::pack(o[2], o[3]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (e + j < b.E) {
+                if constexpr (T::size == 4) static_cast<float*>(dlogits)[at + j] = o[j];
+                else static_cast<uint16_t*>(dlogits)[at + j] = T::one(o[j]);
+              }
+          }
+        }
+      }
+    }
+  }
+}
+
+// Lanes per row: the fewest (a power of two) that cover E four at a time.
+static inline int balance_lanes(int E) {
+  int l = 1;
+  while (l < 32 && l * 4 < E) l <<= 1;
+  return l;
+}
+// Tokens per block of the forward: about four blocks an SM, whole warps of rows.
+static inline int balance_chunk(int T, int E) {
+  const int step = kBalWarps * (32 / balance_lanes(E));
+  return std::max(1, (int)(((long long)T + 148ll * 4 * step - 1) / (148ll * 4 * step))) * step;
+}
+
+struct BalanceScratch {
+  uint32_t* status;
+  BalancePieces pieces;
+  double* dots;
+};
+static BalanceScratch carve_balance(Carver& c, int T, int E, int S) {
+  BalanceScratch w;
+  const int chunk = balance_chunk(T, E);
+  const size_t pieces = (size_t)((T + chunk - 1) / chunk) + (size_t)S;
+  w.status = c.take<uint32_t>(64);
+  w.pieces.status = w.status;
+  w.pieces.probs = c.take<float>(pieces * E);
+  w.pieces.counts = c.take<int32_t>(pieces * E);
+  w.pieces.tokens = c.take<int32_t>(pieces);
+  w.dots = c.take<double>((size_t)S * ((E + 31) / 32));
+  return w;
+}
+
+static nvfp4_status check_balance(const char* name, const void* logits, int dtype, int T, int E, long long stride,
+                                  int k, int score, int S, const int32_t* seq_offsets) {
+  NV_REQUIRE(mx_dtype_ok(dtype), NVFP4_ERR_INVALID_ARG, "%s: unknown dtype %d", name, dtype);
+  NV_REQUIRE(score == MOE_BALANCE_SIGMOID || score == MOE_BALANCE_SOFTMAX, NVFP4_ERR_INVALID_ARG,
+             "%s: unknown score %d", name, score);
+  NV_REQUIRE(T >= 0 && S >= 1, NVFP4_ERR_INVALID_ARG, "%s: T=%d S=%d", name, T, S);
+  NV_REQUIRE(T <= (1 << 30) && S <= (1 << 24), NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: T=%d or S=%d is too large", name, T,
+             S);
+  NV_REQUIRE(E >= 1 && E <= kBalMaxE && k >= 1 && k <= kBalMaxK, NVFP4_ERR_UNSUPPORTED_SHAPE,
+             "%s: needs 1 <= E <= %d and 1 <= k <= %d (E=%d k=%d)", name, kBalMaxE, kBalMaxK, E, k);
+  NV_REQUIRE(seq_offsets || S == 1, NVFP4_ERR_INVALID_ARG, "%s: S=%d sequences need seq_offsets", name, S);
+  NV_REQUIRE(T == 0 || logits, NVFP4_ERR_INVALID_ARG, "%s: logits is NULL", name);
+  NV_REQUIRE(T <= 1 || stride >= E, NVFP4_ERR_INVALID_ARG, "%s: row stride %lld is below E=%d", name, stride, E);
+  NV_REQUIRE(aligned(logits, mx_elem_size(dtype)) && aligned(seq_offsets, 4), NVFP4_ERR_INVALID_ARG,
+             "%s: a tensor is not aligned to its elements", name);
+  return NVFP4_OK;
+}
+
+// Calls f(type tag, vector loads allowed, logits per lane / 4).
+template <typename F>
+static nvfp4_status with_balance(int dtype, bool vec, int E, F&& f) {
+  auto by_v = [&](auto tag, auto v) -> nvfp4_status {
+    if (E <= 128) return f(tag, v, std::integral_constant<int, 1>{});
+    if (E <= 256) return f(tag, v, std::integral_constant<int, 2>{});
+    if (E <= 512) return f(tag, v, std::integral_constant<int, 4>{});
+    return f(tag, v, std::integral_constant<int, 8>{});
+  };
+  auto by_vec = [&](auto tag) -> nvfp4_status {
+    return vec ? by_v(tag, std::true_type{}) : by_v(tag, std::false_type{});
+  };
+  if (dtype == MXFP4_DTYPE_BF16) return by_vec(Bf16{});
+  if (dtype == MXFP4_DTYPE_F16) return by_vec(F16{});
+  return by_vec(F32{});
+}
+// Whether rows may be read or written four elements at a time.
+static inline bool balance_vec(const void* p, long long stride, int T, int E, int elem) {
+  return E % 4 == 0 && row_access_bytes(p, T > 1 ? stride * elem : 0, elem) >= 4 * elem;
+}
+
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" size_t moe_balance_loss_workspace_size(int T, int E, int S) {
+  if (T < 0 || T > (1 << 30) || E < 1 || E > kBalMaxE || S < 1 || S > (1 << 24)) return 0;
+  Carver c(nullptr);
+  carve_balance(c, T, E, S);
+  return c.size();
+}
+
+extern "C" nvfp4_status moe_balance_loss(const void* logits, int dtype, int T, int E, long long row_stride,
+                                         const int32_t* topk_idx, int k, int score, const uint8_t* token_mask,
+                                         const int32_t* seq_offsets, int S, float coeff, float* loss, int32_t* counts,
+                                         int32_t* tokens, float* probs, void* ws, size_t ws_bytes, void* stream) {
+  NV_CHECK(check_balance("moe_balance_loss", logits, dtype, T, E, row_stride, k, score, S, seq_offsets));
+  NV_REQUIRE((T == 0 || topk_idx) && loss && counts && tokens && probs, NVFP4_ERR_INVALID_ARG,
+             "moe_balance_loss: a required pointer is NULL");
+  NV_REQUIRE(aligned(topk_idx, 4) && aligned(loss, 4) && aligned(counts, 4) && aligned(tokens, 4) && aligned(probs, 4),
+             NVFP4_ERR_INVALID_ARG, "moe_balance_loss: a tensor is not aligned to its elements");
+  const size_t need = moe_balance_loss_workspace_size(T, E, S);
+  NV_REQUIRE(ws && ws_bytes >= need && aligned(ws, 256), NVFP4_ERR_WORKSPACE,
+             "moe_balance_loss: needs a 256-byte aligned workspace of %zu bytes", need);
+  int sms = 0;
+  NV_CHECK(device_sm_count(&sms));
+  cudaStream_t s = as_stream(stream);
+  Carver c(ws);
+  const BalanceScratch w = carve_balance(c, T, E, S);
+  const int chunk = balance_chunk(T, E);
+  const BalanceShape b{T, E, S, k, score, balance_lanes(E), row_stride, seq_offsets, token_mask};
+  const dim3 grid((unsigned)std::max(1, (T + chunk - 1) / chunk));
+  const size_t smem = (size_t)(kBalWarps + 1) * E * 4;
+  NV_CHECK(with_balance(dtype, balance_vec(logits, row_stride, T, E, mx_elem_size(dtype)), E,
+                        [&](auto tag, auto vec, auto v) -> nvfp4_status {
+                          constexpr int V = decltype(v)::value, UR = V == 1 ? 4 : V == 2 ? 2 : 1;
+                          return launch_dependent("balance_pieces_kernel",
+                                                  balance_pieces_kernel<decltype(tag), decltype(vec)::value, V, UR>,
+                                                  grid, dim3(kBalThreads), smem, s, logits, topk_idx, b, chunk,
+                                                  w.pieces);
+                        }));
+  return launch_dependent("balance_finish_kernel", balance_finish_kernel, dim3((unsigned)S, (unsigned)((E + 31) / 32)),
+                          dim3(kBalThreads), 0, s, b, chunk, w.pieces, w.dots, coeff, loss, counts, tokens, probs);
+}
+
+extern "C" nvfp4_status moe_balance_loss_backward(const void* logits, int dtype, int T, int E, long long row_stride,
+                                                  int k, int score, const uint8_t* token_mask,
+                                                  const int32_t* seq_offsets, int S, float coeff,
+                                                  const int32_t* counts, const int32_t* tokens,
+                                                  const float* grad_loss, void* dlogits, long long grad_stride,
+                                                  void* stream) {
+  NV_CHECK(check_balance("moe_balance_loss_backward", logits, dtype, T, E, row_stride, k, score, S, seq_offsets));
+  if (T == 0) return NVFP4_OK;
+  NV_REQUIRE(counts && tokens && grad_loss && dlogits, NVFP4_ERR_INVALID_ARG,
+             "moe_balance_loss_backward: a required pointer is NULL");
+  NV_REQUIRE(T <= 1 || grad_stride >= E, NVFP4_ERR_INVALID_ARG,
+             "moe_balance_loss_backward: gradient stride %lld is below E=%d", grad_stride, E);
+  NV_REQUIRE(aligned(dlogits, mx_elem_size(dtype)) && aligned(counts, 4) && aligned(tokens, 4) &&
+                 aligned(grad_loss, 4),
+             NVFP4_ERR_INVALID_ARG, "moe_balance_loss_backward: a tensor is not aligned to its elements");
+  int sms = 0;
+  NV_CHECK(device_sm_count(&sms));
+  const BalanceShape b{T, E, S, k, score, balance_lanes(E), row_stride, seq_offsets, token_mask};
+  const int elem = mx_elem_size(dtype);
+  const bool vec = balance_vec(logits, row_stride, T, E, elem) && balance_vec(dlogits, grad_stride, T, E, elem);
+  // about eight blocks an SM; a warp takes neighbouring rows, so that it
+  // seldom changes sequence
+  const int per_iter = 32 / b.lanes;
+  const long long warps = (long long)sms * 8 * kBalWarps;
+  const int rows_per_warp = (int)(((T + warps - 1) / warps + per_iter - 1) / per_iter) * per_iter;
+  const long long rows_per_block = (long long)rows_per_warp * kBalWarps;
+  const dim3 grid((unsigned)((T + rows_per_block - 1) / rows_per_block));
+  return with_balance(dtype, vec, E, [&](auto tag, auto vv, auto v) -> nvfp4_status {
+    constexpr int V = decltype(v)::value, UR = V == 1 ? 4 : V == 2 ? 2 : 1;
+    return launch_dependent("balance_backward_kernel",
+                            balance_backward_kernel<decltype(tag), decltype(vv)::value, V, UR>, grid,
+                            dim3(kBalThreads), 0, as_stream(stream), logits, b, rows_per_warp, coeff, counts, tokens,
+                            grad_loss, dlogits, grad_stride);
+  });
+}

@@ -1,0 +1,435 @@
+"""MXFP4 quantisers, read-back and products against the 64-bit oracle."""
+import numpy as np
+import pytest
+import torch
+
+from _util import capi, require_cuda
+from oracle import mxfp4
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def matrix(rows, cols, dtype, seed=0, special=True):
+    """Normal rows with outliers; the first rows hold the awkward values."""
+    g = torch.Generator().manual_seed(seed + 7919 * rows + cols)
+    x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-12, 6, (rows, 1), generator=g).float())
+    x = torch.where(torch.rand(rows, cols, generator=g) < 0.01, 30 * x, x)
+    if special:
+        tiny = torch.finfo(dtype).smallest_normal
+        if rows > 3:
+            x[0] = 0.0
+            x[1] = torch.arange(cols).float() % 64 / 8 - 4                   # ties
+            x[2] = tiny * (torch.arange(cols).float() % 5 - 2)
+            x[3, cols // 2] = torch.finfo(dtype).max
+        if rows > 6:
+            x[4, cols // 3] = float("inf")
+            x[5, cols - 1] = float("nan")
+            x[6, 0] = -float("inf")
+            x[6, 1:] = -0.0
+    return x.to(dtype)
+
+
+def check_quantized(q, x, layout):
+    """Codes and scale bytes equal the oracle's for the rows of x."""
+    rows, cols = x.shape
+    codes, scales = mxfp4.quantize(np64(x))
+    got = q.codes.cpu().numpy().reshape(rows, -1)
+    assert np.array_equal(got, codes)
+    s = q.scales.cpu().numpy().reshape(-1)
+    if layout == "canonical":
+        assert np.array_equal(s.reshape(scales.shape), scales)
+    else:
+        assert np.array_equal(s[mxfp4.tiled_index(rows, cols)], scales)
+        # padding blocks of data rows are zero
+        pad = -(-scales.shape[1] // 4) * 4
+        assert (s[mxfp4.tiled_index(rows, pad * 32)[:, scales.shape[1]:]] == 0).all()
+
+
+SHAPES = [(1, 1), (1, 32), (3, 33), (16, 256), (129, 100), (7, 2049), (130, 128), (300, 514), (5000, 300), (64, 6144)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("layout", ["tiled", "canonical"])
+def test_quantize_matches_oracle(rows, cols, dtype, layout):
+    require_cuda()
+    c = capi()
+    x = matrix(rows, cols, DTYPES[dtype])
+    check_quantized(c.mxfp4_quantize(x.cuda(), layout), x, layout)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + [(1, 700), (31, 64), (513, 96), (1030, 65)])
+@pytest.mark.parametrize("layout", ["tiled", "canonical"])
+def test_quantize_transposed_matches_oracle(rows, cols, dtype, layout):
+    require_cuda()
+    c = capi()
+    x = matrix(cols, rows, DTYPES[dtype]).t().contiguous()
+    check_quantized(c.mxfp4_quantize_transposed(x.cuda(), layout), x.t(), layout)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("off,pad", [(0, 8), (0, 4), (0, 2), (0, 1), (8, 16), (4, 12), (2, 6), (1, 7)])
+def test_strided_rows_of_every_alignment(dtype, off, pad):
+    """Rows at every offset and pitch alignment: the access width changes, the
+    result does not, and nothing outside the rows is read into it."""
+    require_cuda()
+    c = capi()
+    rows, cols = 70, 200
+    x = matrix(rows, cols, DTYPES[dtype])
+    big = torch.full((rows, off + cols + pad), float("nan"), dtype=DTYPES[dtype], device="cuda")
+    view = big[:, off:off + cols]
+    view.copy_(x)
+    check_quantized(c.mxfp4_quantize(view), x, "tiled")
+    check_quantized(c.mxfp4_quantize_transposed(view), x.t(), "tiled")
+    # read-back into the same strided rows leaves the rest alone
+    q = c.mxfp4_quantize(view)
+    c.mxfp4_dequantize(q, out=view)
+    want = mxfp4.dequantize(*mxfp4.quantize(np64(x)), cols)
+    want = torch.from_numpy(want).to(DTYPES[dtype]).double().numpy()
+    assert np.array_equal(np64(view), want, equal_nan=True)
+    rest = np64(big)
+    assert np.isnan(rest[:, :off]).all() and np.isnan(rest[:, off + cols:]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("layout", ["tiled", "canonical"])
+def test_dequantize_every_code_and_scale(rows, cols, dtype, layout):
+    require_cuda()
+    c = capi()
+    rng = np.random.default_rng(rows * 31 + cols)
+    codes = rng.integers(0, 256, (rows, -(-cols // 32) * 16), dtype=np.uint8)
+    scales = rng.integers(0, 256, (rows, -(-cols // 32)), dtype=np.uint8)
+    s = scales if layout == "canonical" else mxfp4.to_tiled(scales, cols)
+    q = c.Mxfp4(torch.from_numpy(codes).cuda(), torch.from_numpy(s.copy()).cuda(), rows, cols, layout)
+    v = torch.from_numpy(mxfp4.dequantize(codes, scales, cols))
+    got = c.mxfp4_dequantize(q, dtype=DTYPES[dtype])
+    # one rounding from the exact value (fp64 -> fp32 is exact or overflows like the product does)
+    assert torch.equal(torch.nan_to_num(got.cpu().float(), nan=-77.0),
+                       torch.nan_to_num(v.float().to(DTYPES[dtype]).float(), nan=-77.0))
+    if dtype != "fp16":
+        fine = v.abs() <= torch.finfo(DTYPES[dtype]).max
+        assert torch.equal(got.cpu().double()[fine], v[fine])
+
+
+def test_quantize_gathers_rows():
+    require_cuda()
+    c = capi()
+    x = matrix(9, 100, torch.bfloat16)
+    perm = torch.tensor([3, -1, 8, 8, 9, 0, 2 ** 31 - 1, -2 ** 31, 7] * 20, dtype=torch.int32)
+    q = c.mxfp4_quantize(x.cuda(), perm=perm.cuda())
+    rows = torch.zeros(perm.numel(), 100, dtype=torch.bfloat16)
+    ok = (perm >= 0) & (perm < 9)
+    rows[ok] = x[perm[ok].long()]
+    check_quantized(q, rows, "tiled")
+    empty = c.mxfp4_quantize(x.cuda(), perm=perm[:0].cuda())
+    assert empty.rows == 0
+
+
+def test_zero_rows_and_stacks():
+    require_cuda()
+    c = capi()
+    q = c.mxfp4_quantize(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"))
+    assert c.mxfp4_dequantize(q).shape == (0, 64)
+    w = matrix(256, 96, torch.bfloat16, special=False).reshape(2, 128, 96)
+    check_quantized(c.mxfp4_quantize(w.cuda()), w.reshape(256, 96), "tiled")
+    y = c.mxfp4_matmul(q, c.mxfp4_quantize(w[0, :, :64].cuda()))
+    assert y.shape == (0, 128)
+    assert c.mxfp4_linear(torch.zeros(0, 64, device="cuda"), c.mxfp4_quantize(w[0, :, :64].cuda())).shape == (0, 128)
+
+
+# --- products ----------------------------------------------------------------
+
+def operand(rows, cols, seed, integers=False):
+    """(Mxfp4 on the device, its float64 values)."""
+    c = capi()
+    rng = np.random.default_rng(seed)
+    if integers:
+        x = rng.choice([-6.0, -4, -3, -2, -1, 0, 1, 2, 3, 4, 6], (rows, cols))
+        x[:, ::32] = 4.0                       # every block's scale is 1
+    else:
+        x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-6, 6, (rows, 1)))
+    codes, scales = mxfp4.quantize(x)
+    q = c.Mxfp4(torch.from_numpy(codes).cuda(), torch.from_numpy(mxfp4.to_tiled(scales, cols)).cuda(), rows, cols)
+    return q, mxfp4.dequantize(codes, scales, cols)
+
+
+def product_bound(a, b, ref, dtype, row_weight=None, bias=None):
+    """Largest possible |y - ref|: the products of E2M1 values are exact; K of
+    them enter fp32 sums in some order, each addition off by at most 2^-23
+    (truncated) of a partial sum that never passes sum |a||b|; bias and
+    row_weight round once each; the store by half a step of the output type
+    (or half its smallest subnormal)."""
+    K = a.shape[1]
+    mag = np.abs(a) @ np.abs(b).T
+    if bias is not None:
+        mag = mag + np.abs(bias)
+    err = (K + 2) * 2.0 ** -23 * mag
+    if row_weight is not None:
+        err = err * np.abs(row_weight)[:, None] + 2.0 ** -24 * np.abs(ref)
+    fi = torch.finfo(dtype)
+    return err + fi.eps / 2 * (np.abs(ref) + err) + fi.smallest_normal * fi.eps
+
+
+MNK = [(1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16, 256, 128), (17, 500, 160),
+       (31, 64, 256), (32, 129, 288), (33, 1000, 544), (64, 384, 1024), (65, 128, 100), (100, 300, 2048),
+       (128, 128, 512), (129, 255, 320), (200, 1024, 640), (256, 256, 256), (257, 130, 224), (300, 700, 384),
+       (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000)]
+
+
+@pytest.mark.parametrize("M,N,K", MNK)
+def test_matmul_matches_oracle(M, N, K):
+    require_cuda()
+    c = capi()
+    a, av = operand(M, K, M + N)
+    b, bv = operand(N, K, M + K + 1)
+    ref = av @ bv.T
+    for name, dt in DTYPES.items():
+        y = c.mxfp4_matmul(a, b, out_dtype=dt)
+        assert y.dtype == dt
+        if name == "fp16":
+            keep = np.abs(ref) < 60000
+            assert (np.abs(np64(y) - ref)[keep] <= product_bound(av, bv, ref, dt)[keep]).all()
+        else:
+            assert (np.abs(np64(y) - ref) <= product_bound(av, bv, ref, dt)).all(), name
+
+
+@pytest.mark.parametrize("M,N,K", MNK)
+def test_matmul_of_integers_is_exact(M, N, K):
+    """Integer values: every partial sum is an integer below 2^24, so fp32
+    accumulation has no rounding and the output is the product itself."""
+    require_cuda()
+    c = capi()
+    a, av = operand(M, K, 3 * M + N, integers=True)
+    b, bv = operand(N, K, 5 * N + K, integers=True)
+    ref = av @ bv.T
+    assert np.abs(ref).max() < 2 ** 24 and 36 * K < 2 ** 24
+    y = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
+    assert np.array_equal(np64(y), ref)
+
+
+def test_matmul_bias_row_weight_and_strided_out():
+    require_cuda()
+    c = capi()
+    rng = np.random.default_rng(5)
+    for M, N, K in [(3, 200, 320), (40, 130, 96), (300, 300, 256)]:
+        a, av = operand(M, K, 1)
+        b, bv = operand(N, K, 2)
+        bias = rng.standard_normal(N).astype(np.float32)
+        rw = rng.standard_normal(M).astype(np.float32)
+        rw[0] = 0.0
+        ref = rw[:, None].astype(np.float64) * (av @ bv.T + bias)
+        big = torch.full((M, N + 13), 7.0, device="cuda")
+        y = c.mxfp4_matmul(a, b, out=big[:, 5:5 + N], bias=torch.from_numpy(bias).cuda(),
+                           row_weight=torch.from_numpy(rw).cuda())
+        assert (np.abs(np64(y) - ref) <= product_bound(av, bv, ref, torch.float32, rw, bias)).all()
+        assert (big[:, :5] == 7.0).all() and (big[:, 5 + N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_a_nan_block_reaches_its_row_only(M):
+    require_cuda()
+    c = capi()
+    a, av = operand(M, 300, 3)
+    b, bv = operand(200, 300, 4)
+    clean = c.mxfp4_matmul(a, b)
+    at = int(mxfp4.tiled_index(M, 300)[M - 1, 9])              # the last, partly filled block
+    a.scales[at] = 255
+    y = c.mxfp4_matmul(a, b)
+    assert torch.isnan(y[M - 1]).all() and torch.equal(y[:M - 1], clean[:M - 1])
+    a.scales[at] = 127
+    b.scales[int(mxfp4.tiled_index(200, 300)[131, 0])] = 255
+    y = c.mxfp4_matmul(a, b)
+    assert torch.isnan(y[:, 131]).all() and not torch.isnan(y[:, :131]).any() and not torch.isnan(y[:, 132:]).any()
+
+
+def test_padding_bytes_do_not_matter():
+    """Scale bytes of padding rows may hold anything, NaN included."""
+    require_cuda()
+    c = capi()
+    for M, N, K in [(3, 70, 100), (150, 260, 300)]:
+        a, av = operand(M, K, 8)
+        b, bv = operand(N, K, 9)
+        want = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
+        for q, rows in ((a, M), (b, N)):
+            keep = torch.zeros_like(q.scales, dtype=torch.bool)
+            keep[torch.from_numpy(mxfp4.tiled_index(rows, -(-K // 128) * 128).reshape(-1)).cuda()] = True
+            q.scales[~keep] = 255
+        assert torch.equal(c.mxfp4_matmul(a, b, out_dtype=torch.float32), want)
+
+
+def grouped_case(counts, gaps, N, K, seed):
+    """Rows in 128-row segments, E matrices of N rows."""
+    segs = [-(-n // 128) * 128 + 128 * g for n, g in zip(counts, gaps)]
+    off = np.concatenate([[0], np.cumsum(segs)]).astype(np.int32)
+    M = int(off[-1])
+    a, av = operand(M, K, seed)
+    b, bv = operand(len(counts) * N, K, seed + 1)
+    return off, M, a, av, b, bv
+
+
+@pytest.mark.parametrize("counts,gaps,N,K", [
+    ([5], [0], 128, 64),
+    ([0, 1, 128, 129, 0, 300, 7], [0, 0, 0, 1, 1, 0, 2], 256, 288),
+    ([3] * 40, [0] * 40, 128, 512),
+    ([1000, 0, 257], [0, 0, 0], 384, 160),
+    ([0, 0, 0], [0, 1, 0], 128, 96),
+])
+def test_grouped_matmul(counts, gaps, N, K):
+    require_cuda()
+    c = capi()
+    off, M, a, av, b, bv = grouped_case(counts, gaps, N, K, 11)
+    E = len(counts)
+    rng = np.random.default_rng(0)
+    rw = rng.standard_normal(M).astype(np.float32)
+    bias = rng.standard_normal(E * N).astype(np.float32)
+    cu = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    for with_counts in (True, False):
+        n = np.array(counts, np.int32) if with_counts else np.diff(off).astype(np.int32)
+        ref = np.full((M, N), -3.0)
+        bound = np.zeros((M, N))
+        for e in range(E):
+            r, w = slice(off[e], off[e] + n[e]), slice(e * N, (e + 1) * N)
+            ref[r] = rw[r, None].astype(np.float64) * (av[r] @ bv[w].T + bias[w])
+            bound[r] = product_bound(av[r], bv[w], ref[r], torch.bfloat16, rw[r], bias[w])
+        out = torch.full((M, N), -3.0, dtype=torch.bfloat16, device="cuda")
+        y = c.mxfp4_matmul(a, b, out=out, bias=cu(bias), row_weight=cu(rw), expert_offsets=cu(off),
+                           expert_counts=cu(n) if with_counts else None)
+        # rows of no expert hold -3 still
+        assert (np.abs(np64(y) - ref) <= bound).all()
+
+
+def test_grouped_offsets_outside_the_rows_are_clamped():
+    require_cuda()
+    c = capi()
+    a, av = operand(256, 64, 1)
+    b, bv = operand(3 * 128, 64, 2)
+    off = torch.tensor([-128, 128, 1 << 30, 0], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([1 << 30, 1 << 30, -5], dtype=torch.int32, device="cuda")
+    y = np64(c.mxfp4_matmul(a, b, out_dtype=torch.float32, expert_offsets=off, expert_counts=cnt))
+    ref = np.concatenate([av[:128] @ bv[:128].T, av[128:] @ bv[128:256].T])
+    assert (np.abs(y - ref) <= 66 * 2.0 ** -23 * 64 * 36 * np.abs(av).max() * np.abs(bv).max()).all()
+
+
+def test_linear_is_quantize_then_matmul():
+    require_cuda()
+    c = capi()
+    for M, N, K, dt in [(1, 300, 6144, torch.bfloat16), (37, 501, 201, torch.float16), (700, 256, 500, torch.float32)]:
+        x = matrix(M, K + 24, dt, special=False).cuda()[:, 8:8 + K]
+        w, _ = operand(N, K, N)
+        y = c.mxfp4_linear(x, w)
+        assert y.dtype == dt
+        assert torch.equal(y, c.mxfp4_matmul(c.mxfp4_quantize(x), w, out_dtype=dt))
+        perm = torch.randint(-1, M, (2 * M + 1,), dtype=torch.int32, device="cuda")
+        yp = c.mxfp4_linear(x, w, perm=perm)
+        assert torch.equal(yp, c.mxfp4_matmul(c.mxfp4_quantize(x, perm=perm), w, out_dtype=dt))
+        assert not yp[perm < 0].any()
+
+
+def test_results_do_not_change_from_run_to_run():
+    require_cuda()
+    c = capi()
+    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024)]:
+        a, _ = operand(M, K, 1)
+        b, _ = operand(N, K, 2)
+        first = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
+        for _ in range(5):
+            assert torch.equal(c.mxfp4_matmul(a, b, out_dtype=torch.float32), first)
+
+
+def test_side_stream_and_captured_graphs_sharing_a_workspace():
+    require_cuda()
+    c = capi()
+    w, _ = operand(500, 640, 1)
+    xs = [matrix(m, 640, torch.bfloat16, special=False).cuda() for m in (3, 200)]
+    want = [c.mxfp4_linear(x, w) for x in xs]
+    ws = torch.empty(c.mxfp4_linear_workspace_size(200, 640), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [c.mxfp4_linear(x, w, workspace=ws) for x in xs]
+    side.synchronize()
+    assert all(torch.equal(g, v) for g, v in zip(got, want))
+    outs = [torch.zeros_like(v) for v in want]
+    graphs = []
+    for x, o in zip(xs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.mxfp4_linear(x, w, out=o, workspace=ws)
+        graphs.append(g)
+    for x in xs:
+        x.mul_(2.0)                                            # powers of two: the outputs double exactly
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, 2 * v) for o, v in zip(outs, want))
+    c.nvfp4_workspace_status(ws)
+
+
+def test_linear_gradients_against_the_formula_and_differences():
+    """y = q(x) q(w)^T; dx = q(dy) q(w^T)^T and dw = q(dy^T) q(x^T)^T from the
+    transposed quantiser, against their formulas in 64 bits.  With operands on
+    the E2M1 grid quantisation changes nothing, so dx and dw are the true
+    gradients of sum(dy * y): checked against exact differences (y is linear
+    in each of x and w)."""
+    require_cuda()
+    c = capi()
+    rng = np.random.default_rng(3)
+    M, N, K = 70, 96, 200
+    grid = np.array([-6.0, -4, -3, -2, -1.5, -1, -0.5, 0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    x, w, dy = (rng.choice(grid, s) for s in ((M, K), (N, K), (M, N)))
+    for t in (x, w, dy):
+        t[:, ::16] = 6.0
+        t[::16, :] = 6.0                                     # every block, either way, has scale 1
+    cu = lambda t: torch.from_numpy(t).to(torch.bfloat16).cuda()  # noqa: E731
+    dx = c.mxfp4_matmul(c.mxfp4_quantize(cu(dy)), c.mxfp4_quantize_transposed(cu(w)), out_dtype=torch.float32)
+    dw = c.mxfp4_matmul(c.mxfp4_quantize_transposed(cu(dy)), c.mxfp4_quantize_transposed(cu(x)),
+                        out_dtype=torch.float32)
+    assert np.array_equal(np64(dx), dy @ w) and np.array_equal(np64(dw), dy.T @ x)
+    loss = lambda x_, w_: float((dy * np64(c.mxfp4_linear(cu(x_), c.mxfp4_quantize(cu(w_)),  # noqa: E731
+                                                          out_dtype=torch.float32))).sum())
+    for i, j in ((0, 1), (17, 33), (69, 199)):
+        for arr, g in ((x, dx), (w, dw)):
+            hi, lo = arr.copy(), arr.copy()
+            hi[i, j], lo[i, j] = 2.0, -2.0
+            d = (loss(hi, w) - loss(lo, w) if arr is x else loss(x, hi) - loss(x, lo)) / 4.0
+            assert d == float(g[i, j])
+
+
+def test_binding_refusals():
+    require_cuda()
+    c = capi()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    q = c.mxfp4_quantize(x)
+    bad = [
+        lambda: c.mxfp4_quantize(x.int()), lambda: c.mxfp4_quantize(x.t()), lambda: c.mxfp4_quantize(x[0]),
+        lambda: c.mxfp4_quantize(x[:1].expand(4, 64)), lambda: c.mxfp4_quantize(x, perm=torch.zeros(4, device="cuda")),
+        lambda: c.mxfp4_quantize(x, out=c.mxfp4_quantize(x[:2])),
+        lambda: c.mxfp4_dequantize(q, out=torch.zeros(4, 63, device="cuda")),
+        lambda: c.Mxfp4(q.codes, q.scales[:100], 4, 64), lambda: c.Mxfp4(q.codes, q.scales, 5, 64),
+        lambda: c.Mxfp4(q.codes, q.scales, 4, 64, "staged"),
+        lambda: c.mxfp4_matmul(q, c.mxfp4_quantize(x[:, :32])),
+        lambda: c.mxfp4_matmul(q, c.mxfp4_quantize(x, "canonical")),
+        lambda: c.mxfp4_matmul(q, q, out=torch.zeros(4, 5, device="cuda")),
+        lambda: c.mxfp4_matmul(q, q, bias=torch.zeros(5, device="cuda")),
+        lambda: c.mxfp4_matmul(q, q, row_weight=torch.zeros(4, dtype=torch.float64, device="cuda")),
+        lambda: c.mxfp4_matmul(q, q, expert_counts=torch.zeros(1, dtype=torch.int32, device="cuda")),
+        lambda: c.mxfp4_matmul(q, q, expert_offsets=torch.zeros(4, dtype=torch.int32, device="cuda")),
+        lambda: c.mxfp4_linear(x[:, :32], q),
+        lambda: c.mxfp4_linear(x, q, out=torch.zeros(4, 4, dtype=torch.int32, device="cuda")),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(c.Nvfp4Error):                       # 4 rows an expert: not a multiple of 128
+        c.mxfp4_matmul(q, q, expert_offsets=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(c.Nvfp4Error):
+        c.mxfp4_linear(x, q, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))

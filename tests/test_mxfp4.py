@@ -1,0 +1,183 @@
+"""MXFP4 and the balance loss on the CPU: the oracles against second
+definitions, the binding's and the library's refusals, the headers."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from _util import ROOT, capi
+from oracle import balance, mxfp4
+
+
+# --- oracles -----------------------------------------------------------------
+
+def test_e2m1_rounding_against_the_seven_midpoints():
+    y = np.arange(-9 * 1024, 9 * 1024 + 1) / 1024.0
+    a = np.abs(y)
+    m = ((a > 0.25).astype(int) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
+    assert np.array_equal(mxfp4.round_e2m1(y), m | (np.signbit(y) << 3))
+
+
+def test_mxfp4_scale_and_values():
+    x = np.zeros((7, 40))
+    x[0, 0] = 7.9                      # floor(log2) = 2: scale 1, clamped to 6
+    x[1, :3] = [8.0, 5.0, 0.25]        # scale 2: 4 * 2, 2.5 -> tie to 2, 0.125 -> 0
+    x[2, 33] = -3 * 2.0 ** -140        # below the smallest scale: 2^-127 stays
+    x[3, 1] = np.inf
+    x[4, 39] = np.nan
+    x[5, :2] = [2.0 ** 127 * 1.75, -2.0 ** 120]
+    codes, scales = mxfp4.quantize(x)
+    assert codes.shape == (7, 32) and scales.shape == (7, 2)
+    assert scales[:, 0].tolist() == [127, 128, 0, 255, 0, 252, 0]
+    assert scales[:, 1].tolist() == [0, 0, 0, 0, 255, 0, 0]
+    v = mxfp4.dequantize(codes, scales, 40)
+    assert v[0, 0] == 6.0 and v[1, :3].tolist() == [8.0, 4.0, 0.0]
+    assert v[2, 33] == 0.0 and np.isnan(v[3, :32]).all() and (v[3, 32:] == 0).all() and np.isnan(v[4, 32:]).all()
+    assert v[5, 0] == 6 * 2.0 ** 125 and (v[6] == 0).all()
+    # quantising the values again changes nothing
+    ok = np.array([0, 1, 2, 5, 6])
+    assert np.array_equal(mxfp4.dequantize(*mxfp4.quantize(v[ok]), 40), v[ok])
+
+
+def test_mxfp4_error_is_within_half_a_step():
+    x = np.random.default_rng(0).standard_normal((50, 320)) * 3
+    codes, scales = mxfp4.quantize(x)
+    v = mxfp4.dequantize(codes, scales, 320)
+    s = np.repeat(np.ldexp(1.0, scales.astype(int) - 127), 32, axis=1)
+    y = np.abs(x) / s
+    assert (y < 8).all()
+    # half the local spacing (0.25, 0.5, 1), or the distance to 6 where clamped
+    half = np.where(y > 6, y - 6, np.where(y > 4, 1.0, np.where(y > 2, 0.5, 0.25)))
+    assert (np.abs(v - x) <= half * s * (1 + 1e-12)).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_balance_gradient_against_differences(score):
+    rng = np.random.default_rng(1)
+    T, E, k = 12, 6, 2
+    l = rng.standard_normal((T, E)) * 2
+    l[3, 2] = -np.inf
+    idx = np.argsort(-l, axis=1)[:, :k]
+    mask = np.ones(T, bool)
+    mask[5] = False
+    off = np.array([0, 4, 4, 9, 11])           # an empty sequence; token 11 in none
+    args = (idx, 0.3, score, mask, off)
+    ref = balance.balance_loss(l, *args)
+    assert ref["tokens"].tolist() == [4, 0, 4, 2, 3]
+    assert (ref["dlogits"][5] == 0).all() and (ref["dlogits"][11] == 0).all() and ref["dlogits"][3, 2] == 0
+    h = 1e-6
+    for t in range(T):
+        for e in range(E):
+            if np.isinf(l[t, e]):
+                continue
+            up, dn = l.copy(), l.copy()
+            up[t, e] += h
+            dn[t, e] -= h
+            num = (balance.balance_loss(up, *args)["loss"] - balance.balance_loss(dn, *args)["loss"]) / (2 * h)
+            # central difference: h^2 |f'''| / 6 and the loss's rounding over 2 h
+            assert abs(num - ref["dlogits"][t, e]) <= 1e-9
+
+
+def test_balance_of_uniform_routing_is_coeff():
+    """Equal counts and equal shares: <f, P> = E * (1/E) = 1 per sequence."""
+    E, k = 8, 2
+    idx = np.array([[(2 * t) % E, (2 * t + 1) % E] for t in range(16)])
+    for score in ("softmax", "sigmoid"):
+        r = balance.balance_loss(np.zeros((16, E)), idx, 0.01, score)
+        assert abs(r["loss"] - 0.01) < 1e-15 and np.abs(r["dlogits"]).max() < 1e-18
+
+
+# --- refusals ----------------------------------------------------------------
+
+FAKE = ctypes.c_void_p(0x1000)
+
+
+def test_quantiser_refusals():
+    lib = capi().lib
+    q = lambda x=FAKE, dt=0, r=4, c=64, st=64, perm=None, n=0, lay=1, co=FAKE, sc=FAKE: \
+        lib.mxfp4_quantize(x, dt, r, c, st, perm, n, lay, co, sc, None)  # noqa: E731
+    assert q(x=None) == 1 and b"NULL" in lib.nvfp4_last_error()
+    assert q(dt=3) == 1 and q(r=-1) == 1 and q(c=0) == 1 and q(st=63) == 1 and q(lay=2) == 1
+    assert q(co=None) == 1 and q(sc=None) == 1 and q(co=ctypes.c_void_p(0x1008)) == 1
+    assert q(x=ctypes.c_void_p(0x1001)) == 1 and q(perm=FAKE, n=-1) == 1
+    assert q(c=(1 << 30) + 1, st=1 << 31) == 2
+    assert q(r=(1 << 31) - 1, c=1 << 20, st=1 << 20) == 2            # 2^51 elements
+    assert q(r=0) == 0 and q(perm=FAKE, n=0) == 0                      # nothing to do
+    t = lambda r=4, c=64, st=64, lay=1, dt=0: \
+        lib.mxfp4_quantize_transposed(FAKE, dt, r, c, st, lay, FAKE, FAKE, None)  # noqa: E731
+    assert t(r=0) == 1 and t(lay=2) == 1 and t(st=1) == 1 and t(dt=-1) == 1 and t(r=(1 << 31) - 1) == 2
+    d = lambda r=4, c=64, st=64, lay=1, dt=0, o=FAKE: \
+        lib.mxfp4_dequantize(FAKE, FAKE, lay, r, c, dt, o, st, None)  # noqa: E731
+    assert d(o=None) == 1 and d(lay=3) == 1 and d(st=5) == 1 and d(r=0) == 0
+    # sizes
+    assert lib.mxfp4_scale_bytes(3, 33, 0) == 6 and lib.mxfp4_scale_bytes(3, 33, 1) == 512
+    assert lib.mxfp4_scale_bytes(129, 160, 1) == 2 * 2 * 512 and lib.mxfp4_scale_bytes(1, 32, 2) == 0
+    assert lib.mxfp4_scale_bytes(-1, 32, 1) == 0
+
+
+def test_product_refusals():
+    lib = capi().lib
+
+    def mm(a=FAKE, M=4, b=FAKE, N=128, K=64, E=0, off=None, cnt=None, rw=None, bias=None, dt=0, y=FAKE, st=128,
+           ws=FAKE, n=256):
+        return lib.mxfp4_matmul(a, FAKE, M, b, FAKE, N, K, E, off, cnt, rw, bias, dt, y, st, ws, n, None)
+    assert mm(a=None) == 1 and mm(b=None) == 1 and mm(y=None) == 1
+    assert mm(M=-1) == 1 and mm(N=0) == 1 and mm(K=0) == 1 and mm(dt=3) == 1 and mm(st=127) == 1
+    assert mm(E=2) == 1 and mm(off=FAKE) == 1 and mm(cnt=FAKE) == 1            # E and the offsets go together
+    assert mm(E=2, off=FAKE, N=130, st=130) == 2 and mm(E=1025, off=FAKE) == 2
+    assert mm(a=ctypes.c_void_p(0x1008)) == 1 and mm(y=ctypes.c_void_p(0x1001)) == 1
+    assert mm(n=255) == 5 and mm(ws=None) == 5 and mm(ws=ctypes.c_void_p(0x1010)) == 5
+    assert mm(K=(1 << 30) + 1) == 2
+    assert mm(M=0) == 0
+
+    def lin(x=FAKE, dt=0, r=4, st=64, perm=None, n=0, N=128, K=64, ws=FAKE, wsn=1 << 20):
+        return lib.mxfp4_linear(x, dt, r, st, perm, n, FAKE, FAKE, N, K, 0, None, None, None, None, 0, FAKE, 128, ws,
+                                wsn, None)
+    assert lin(x=None) == 1 and lin(st=63) == 1 and lin(perm=FAKE, n=-2) == 1 and lin(wsn=256) == 5
+    assert lin(r=0) == 0
+    c = capi()
+    assert c.mxfp4_linear_workspace_size(4, 64) == 256 + 256 + 512
+    assert c.mxfp4_linear_workspace_size(-1, 64) == 0
+
+
+def test_balance_refusals():
+    lib = capi().lib
+
+    def f(l=FAKE, dt=2, T=4, E=8, st=8, idx=FAKE, k=2, sc=0, off=None, S=1, loss=FAKE, ws=FAKE, n=1 << 20):
+        return lib.moe_balance_loss(l, dt, T, E, st, idx, k, sc, None, off, S, 0.1, loss, FAKE, FAKE, FAKE, ws, n,
+                                    None)
+    assert f(l=None) == 1 and f(idx=None) == 1 and f(loss=None) == 1 and f(dt=3) == 1 and f(sc=2) == 1
+    assert f(T=-1) == 1 and f(S=0) == 1 and f(S=2) == 1 and f(st=7) == 1 and f(l=ctypes.c_void_p(0x1002)) == 1
+    assert f(E=0) == 2 and f(E=1025, st=1025) == 2 and f(k=0) == 2 and f(k=33) == 2
+    assert f(n=256) == 5 and f(ws=None) == 5
+
+    def b(T=4, E=8, gs=8, d=FAKE, g=FAKE):
+        return lib.moe_balance_loss_backward(FAKE, 2, T, E, 8, 2, 0, None, None, 1, 0.1, FAKE, FAKE, g, d, gs, None)
+    assert b(gs=7) == 1 and b(d=None) == 1 and b(g=None) == 1 and b(E=2000) == 2 and b(T=0) == 0
+    c = capi()
+    assert c.moe_balance_loss_workspace_size(0, 8) > 0 and c.moe_balance_loss_workspace_size(4, 0) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    c = capi()
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: c.mxfp4_quantize(x), lambda: c.mxfp4_quantize_transposed(x),
+                 lambda: c.Mxfp4(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 4, 64),
+                 lambda: c.moe_balance_loss(x.float(), torch.zeros(4, 2, dtype=torch.int32), 0.1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+@pytest.mark.parametrize("header", ["mxfp4.h", "moe_balance.h"])
+@pytest.mark.parametrize("lang", [("c", "-std=c99"), ("c++", "-std=c++17")])
+def test_headers_compile_as_plain_c_and_cpp(header, lang):
+    cc = shutil.which("gcc" if lang[0] == "c" else "g++")
+    if cc is None:
+        pytest.skip("no host compiler")
+    r = subprocess.run([cc, "-fsyntax-only", lang[1], "-Wall", "-Wextra", "-Werror", "-x", lang[0],
+                        os.path.join(ROOT, "include", header)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
