@@ -620,43 +620,44 @@ def moe_nvfp4_down(W: MoeWeights, h_codes, h_scales, expert_offsets, expert_coun
 #: Element types of unquantised matrices (MXFP4_DTYPE_*).
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-
-class _on:
-    """Makes a tensor's device the current one for a call and gives the
-    device's current stream; every tensor of the call must live there."""
-    __slots__ = ("device", "prev", "stream")
-
-    def __init__(self, device, **tensors):
-        self.device = device
-        for name, t in tensors.items():
-            if t is not None and t.device != device:
-                raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        self.prev = cur if cur != self.device.index else -1
-        if self.prev >= 0:
-            torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            torch.cuda.set_device(self.prev)
+# A small call is bound by its host side, so the functions below read each
+# property of a tensor once and take the current stream as the raw handle.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _matrix(t, name: str, dtypes=_DTYPES) -> int:
-    """Row stride (elements) of a CUDA matrix whose rows are contiguous."""
+def _launch(dev: int, fn, *args):
+    """fn(*args, stream) on device ``dev`` and its current stream."""
+    if _current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
+
+
+def _same_device(dev: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors of a call must be on one device: got {t.device} and cuda:{dev}")
+
+
+def _matrix(t, name: str, dtypes=_DTYPES):
+    """(rows, cols, row stride) of a CUDA matrix whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} must be a matrix with at least one column, got shape {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows (stride {tuple(t.stride())})")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} must not have overlapping rows (stride {tuple(t.stride())})")
-    return t.stride(0)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be a matrix with at least one column, got shape {tuple(shape)}")
+    rows, cols = shape
+    if cols > 1 and strides[1] != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride {strides})")
+    if rows > 1 and strides[0] < cols:
+        raise ValueError(f"{name} must not have overlapping rows (stride {strides})")
+    return rows, cols, strides[0]
 
 
 def _vector(t, dtype, name: str, n: int):
@@ -664,6 +665,20 @@ def _vector(t, dtype, name: str, n: int):
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
     return t
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _mx_sizes(rows: int, cols: int, layout: str):
+    """Bytes of (a row's codes, the scales) of an MXFP4 matrix."""
+    blocks = (cols + 31) // 32
+    if layout == "canonical":
+        return blocks * 16, rows * blocks
+    if layout == "tiled":
+        return blocks * 16, (rows + 127) // 128 * ((blocks + 3) // 4) * 512
+    raise ValueError(f"MXFP4 layout must be 'tiled' or 'canonical', got {layout!r}")
 
 
 @dataclass
@@ -680,37 +695,32 @@ class Mxfp4:
     def __post_init__(self):
         _cuda(self.codes, torch.uint8, "codes")
         _cuda(self.scales, torch.uint8, "scales")
-        if self.layout not in ("tiled", "canonical"):
-            raise ValueError(f"MXFP4 layout must be 'tiled' or 'canonical', got {self.layout!r}")
-        blocks = (self.cols + 31) // 32
         if self.rows < 0 or self.cols < 1:
             raise ValueError(f"no MXFP4 matrix has shape {self.rows} x {self.cols}")
-        if self.codes.numel() < self.rows * blocks * 16:
+        row_bytes, scale_bytes = _mx_sizes(self.rows, self.cols, self.layout)
+        if self.codes.numel() < self.rows * row_bytes:
             raise ValueError(f"codes hold {self.codes.numel()} bytes; a {self.rows} x {self.cols} matrix has "
-                             f"{self.rows * blocks * 16}")
-        need = (self.rows * blocks if self.layout == "canonical"
-                else (self.rows + 127) // 128 * ((blocks + 3) // 4) * 512)
-        if self.scales.numel() < need:
-            raise ValueError(f"scales hold {self.scales.numel()} bytes; a {self.rows} x {self.cols} matrix has {need} "
-                             f"({self.layout})")
-        if self.scales.device != self.codes.device:
-            raise ValueError(f"scales must be on {self.codes.device}, got {self.scales.device}")
-
-
-def _mx_empty(rows: int, cols: int, layout: str, device) -> Mxfp4:
-    blocks = (cols + 31) // 32
-    codes = torch.empty((rows, blocks * 16), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, blocks) if layout == "canonical"
-                         else (rows + 127) // 128 * ((blocks + 3) // 4) * 512, dtype=torch.uint8, device=device)
-    return Mxfp4(codes, scales, rows, cols, layout)
+                             f"{self.rows * row_bytes}")
+        if self.scales.numel() < scale_bytes:
+            raise ValueError(f"scales hold {self.scales.numel()} bytes; a {self.rows} x {self.cols} matrix has "
+                             f"{scale_bytes} ({self.layout})")
+        _same_device(self.codes.get_device(), self.scales)
 
 
 def _mx_out(out, rows: int, cols: int, layout: str, device) -> Mxfp4:
-    if out is None:
-        return _mx_empty(rows, cols, layout, device)
-    if (out.rows, out.cols, out.layout) != (rows, cols, layout):
-        raise ValueError(f"out is {out.rows} x {out.cols} ({out.layout}); this call writes {rows} x {cols} ({layout})")
-    return out
+    """The matrix a quantiser writes: ``out``, or a new one."""
+    row_bytes, scale_bytes = _mx_sizes(rows, cols, layout)
+    if out is not None:
+        if (out.rows, out.cols, out.layout) != (rows, cols, layout):
+            raise ValueError(f"out is {out.rows} x {out.cols} ({out.layout}); "
+                             f"this call writes {rows} x {cols} ({layout})")
+        return out
+    q = Mxfp4.__new__(Mxfp4)                       # sizes and devices are right by construction
+    q.codes = torch.empty((rows, row_bytes), dtype=torch.uint8, device=device)
+    q.scales = torch.empty((rows, row_bytes // 16) if layout == "canonical" else scale_bytes, dtype=torch.uint8,
+                           device=device)
+    q.rows, q.cols, q.layout = rows, cols, layout
+    return q
 
 
 def mxfp4_quantize(x: torch.Tensor, layout: str = "tiled", perm: torch.Tensor | None = None,
@@ -722,42 +732,46 @@ def mxfp4_quantize(x: torch.Tensor, layout: str = "tiled", perm: torch.Tensor | 
     if isinstance(x, torch.Tensor) and x.dim() == 3:
         if not x.is_contiguous():
             raise ValueError("a stack of matrices must be contiguous")
-        x = x.reshape(-1, x.shape[2])
-    stride = _matrix(x, "x")
-    rows, cols = x.shape
-    n = rows
-    if perm is not None:
-        n = _cuda(perm, torch.int32, "perm").numel()
+        x = x.flatten(0, 1)
+    rows, cols, stride = _matrix(x, "x")
+    n = rows if perm is None else _cuda(perm, torch.int32, "perm").numel()
     q = _mx_out(out, n, cols, layout, x.device)
-    with _on(x.device, perm=perm, out=q.codes) as stream:
-        _check(lib.mxfp4_quantize(x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride,
-                                  None if perm is None or n == 0 else perm.data_ptr(), n, _LAYOUTS[layout],
-                                  q.codes.data_ptr(), q.scales.data_ptr(), stream) if n else 0)
+    dev = x.get_device()
+    _same_device(dev, perm, q.codes)
+    if n:
+        _launch(dev, lib.mxfp4_quantize, x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride, _ptr(perm), n,
+                _LAYOUTS[layout], q.codes.data_ptr(), q.scales.data_ptr())
     return q
 
 
 def mxfp4_quantize_transposed(x: torch.Tensor, layout: str = "tiled", out: Mxfp4 | None = None) -> Mxfp4:
     """x [rows, cols] -> the MXFP4 matrix of its transpose (cols x rows, the
     blocks along x's columns): the operand of a product that sums over rows."""
-    stride = _matrix(x, "x")
-    rows, cols = x.shape
+    rows, cols, stride = _matrix(x, "x")
+    if rows < 1:
+        raise ValueError("x must have at least one row")
     q = _mx_out(out, cols, rows, layout, x.device)
-    with _on(x.device, out=q.codes) as stream:
-        _check(lib.mxfp4_quantize_transposed(x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride, _LAYOUTS[layout],
-                                             q.codes.data_ptr(), q.scales.data_ptr(), stream))
+    dev = x.get_device()
+    _same_device(dev, q.codes)
+    _launch(dev, lib.mxfp4_quantize_transposed, x.data_ptr(), _DTYPES[x.dtype], rows, cols, stride, _LAYOUTS[layout],
+            q.codes.data_ptr(), q.scales.data_ptr())
     return q
 
 
 def mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
-    """The values of an MXFP4 matrix, [rows, cols] (exact in bf16 and fp32)."""
+    """The values of an MXFP4 matrix, [rows, cols] (exact in bf16 and fp32),
+    in ``dtype``, or in ``out``'s."""
+    codes = q.codes
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    stride = _matrix(out, "out")
-    if tuple(out.shape) != (q.rows, q.cols):
-        raise ValueError(f"out must be {q.rows} x {q.cols}, got {tuple(out.shape)}")
-    with _on(q.codes.device, out=out) as stream:
-        _check(lib.mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), _LAYOUTS[q.layout], q.rows, q.cols,
-                                    _DTYPES[out.dtype], out.data_ptr(), stride, stream))
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=codes.device)
+    rows, cols, stride = _matrix(out, "out")
+    if rows != q.rows or cols != q.cols:
+        raise ValueError(f"out must be {q.rows} x {q.cols}, got {rows} x {cols}")
+    dev = codes.get_device()
+    _same_device(dev, out)
+    if rows:
+        _launch(dev, lib.mxfp4_dequantize, codes.data_ptr(), q.scales.data_ptr(), _LAYOUTS[q.layout], rows, cols,
+                _DTYPES[out.dtype], out.data_ptr(), stride)
     return out
 
 
@@ -765,32 +779,32 @@ def _product_args(M: int, b: Mxfp4, out_dtype, out, bias, row_weight, expert_off
     """Checks a product's tensors; returns (E, N, out, its row stride)."""
     if b.layout != "tiled":
         raise ValueError("a product takes tiled scales; quantise with layout='tiled'")
-    E = 0
+    E, N = 0, b.rows
     if expert_offsets is not None:
         E = _cuda(expert_offsets, torch.int32, "expert_offsets").numel() - 1
-        if E < 1 or b.rows % E:
-            raise ValueError(f"expert_offsets of {E + 1} entries do not divide b's {b.rows} rows into experts")
+        if E < 1 or N % E:
+            raise ValueError(f"expert_offsets of {E + 1} entries do not divide b's {N} rows into experts")
+        N //= E
         if expert_counts is not None:
             _vector(expert_counts, torch.int32, "expert_counts", E)
     elif expert_counts is not None:
         raise ValueError("expert_counts go with expert_offsets")
-    N = b.rows // max(E, 1)
+    if N < 1:
+        raise ValueError("b has no rows")
     if row_weight is not None:
         _vector(row_weight, torch.float32, "row_weight", M)
     if bias is not None:
         _vector(bias, torch.float32, "bias", b.rows)
     if out is None:
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype must be one of {', '.join(map(str, _DTYPES))}, got {out_dtype}")
         # grouped: the rows of no expert are not written
-        make = torch.zeros if E else torch.empty
-        out = make((M, N), dtype=out_dtype, device=b.codes.device)
-    stride = _matrix(out, "out")
-    if tuple(out.shape) != (M, N):
-        raise ValueError(f"out must be {M} x {N}, got {tuple(out.shape)}")
+        out = (torch.zeros if E else torch.empty)((M, N), dtype=out_dtype, device=b.codes.device)
+        return E, N, out, N
+    rows, cols, stride = _matrix(out, "out")
+    if rows != M or cols != N:
+        raise ValueError(f"out must be {M} x {N}, got {rows} x {cols}")
     return E, N, out, stride
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def mxfp4_matmul_workspace_size() -> int:
@@ -815,12 +829,11 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out_dtype: torch.dtype = torch.bfloat16, ou
         workspace = _workspace(256, a.codes.device)
     else:
         _cuda(workspace, torch.uint8, "workspace")
-    with _on(a.codes.device, b=b.codes, out=out, bias=bias, row_weight=row_weight, expert_offsets=expert_offsets,
-             expert_counts=expert_counts, workspace=workspace) as stream:
-        _check(lib.mxfp4_matmul(a.codes.data_ptr(), a.scales.data_ptr(), a.rows, b.codes.data_ptr(),
-                                b.scales.data_ptr(), N, a.cols, E, _ptr(expert_offsets), _ptr(expert_counts),
-                                _ptr(row_weight), _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride,
-                                workspace.data_ptr(), workspace.numel(), stream))
+    dev = a.codes.get_device()
+    _same_device(dev, b.codes, out, bias, row_weight, expert_offsets, expert_counts, workspace)
+    _launch(dev, lib.mxfp4_matmul, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, b.codes.data_ptr(),
+            b.scales.data_ptr(), N, a.cols, E, _ptr(expert_offsets), _ptr(expert_counts), _ptr(row_weight),
+            _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride, workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -835,25 +848,23 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4, out_dtype: torch.dtype | None = None
     """mxfp4_matmul with a = x (or, with ``perm``, its rows x[perm[r]])
     quantised in the call.  x is [rows, K], any row stride; the result has
     x's dtype unless ``out_dtype`` or ``out`` says otherwise."""
-    x_stride = _matrix(x, "x")
-    rows, K = x.shape
+    rows, K, x_stride = _matrix(x, "x")
     if K != w.cols:
         raise ValueError(f"x has {K} columns and w {w.cols}")
     M = rows if perm is None else _cuda(perm, torch.int32, "perm").numel()
-    E, N, out, stride = _product_args(M, w, out_dtype or x.dtype, out, bias, row_weight, expert_offsets,
-                                      expert_counts)
-    if M == 0:
-        return out
+    dtype = x.dtype
+    E, N, out, stride = _product_args(M, w, out_dtype or dtype, out, bias, row_weight, expert_offsets, expert_counts)
     if workspace is None:
         workspace = _workspace(lib.mxfp4_linear_workspace_size(M, K), x.device)
     else:
         _cuda(workspace, torch.uint8, "workspace")
-    with _on(x.device, w=w.codes, out=out, bias=bias, row_weight=row_weight, perm=perm,
-             expert_offsets=expert_offsets, expert_counts=expert_counts, workspace=workspace) as stream:
-        _check(lib.mxfp4_linear(x.data_ptr(), _DTYPES[x.dtype], rows, x_stride, _ptr(perm), M, w.codes.data_ptr(),
-                                w.scales.data_ptr(), N, K, E, _ptr(expert_offsets), _ptr(expert_counts),
-                                _ptr(row_weight), _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride,
-                                workspace.data_ptr(), workspace.numel(), stream))
+    dev = x.get_device()
+    _same_device(dev, w.codes, out, bias, row_weight, perm, expert_offsets, expert_counts, workspace)
+    if M:
+        _launch(dev, lib.mxfp4_linear, x.data_ptr(), _DTYPES[dtype], rows, x_stride, _ptr(perm), M,
+                w.codes.data_ptr(), w.scales.data_ptr(), N, K, E, _ptr(expert_offsets), _ptr(expert_counts),
+                _ptr(row_weight), _ptr(bias), _DTYPES[out.dtype], out.data_ptr(), stride, workspace.data_ptr(),
+                workspace.numel())
     return out
 
 
@@ -890,38 +901,36 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
     gives them).  ``token_mask`` (bool or uint8 [T]): tokens to count.
     ``seq_offsets`` (int32 [S + 1]): the loss per sequence, averaged over the
     sequences that have tokens."""
-    stride = _matrix(logits, "logits")
-    T, E = logits.shape
-    _cuda(topk_idx, torch.int32, "topk_idx")
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx must be [{T}, k], got {tuple(topk_idx.shape)}")
-    k = topk_idx.shape[1]
+    T, E, stride = _matrix(logits, "logits")
+    idx_shape = _cuda(topk_idx, torch.int32, "topk_idx").shape
+    if len(idx_shape) != 2 or idx_shape[0] != T:
+        raise ValueError(f"topk_idx must be [{T}, k], got {tuple(idx_shape)}")
     if score not in BALANCE_SCORES:
         raise ValueError(f"score must be one of {', '.join(BALANCE_SCORES)}, got {score!r}")
     if token_mask is not None:
-        if token_mask.dtype == torch.bool:
+        if isinstance(token_mask, torch.Tensor) and token_mask.dtype == torch.bool:
             token_mask = token_mask.view(torch.uint8)
         _vector(token_mask, torch.uint8, "token_mask", T)
     S = 1
     if seq_offsets is not None:
         S = _cuda(seq_offsets, torch.int32, "seq_offsets").numel() - 1
-    if S < 1:
-        raise ValueError("seq_offsets must hold at least two values")
-    dev = logits.device
-    loss = torch.empty(1, dtype=torch.float32, device=dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    tokens = torch.empty(S + 1, dtype=torch.int32, device=dev)
-    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+        if S < 1:
+            raise ValueError("seq_offsets must hold at least two values")
+    device = logits.device
+    loss = torch.empty(1, dtype=torch.float32, device=device)
+    counts = torch.empty((S, E), dtype=torch.int32, device=device)
+    tokens = torch.empty(S + 1, dtype=torch.int32, device=device)
+    probs = torch.empty((S, E), dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = _workspace(lib.moe_balance_loss_workspace_size(T, E, S), dev)
+        workspace = _workspace(lib.moe_balance_loss_workspace_size(T, E, S), device)
     else:
         _cuda(workspace, torch.uint8, "workspace")
-    with _on(dev, topk_idx=topk_idx, token_mask=token_mask, seq_offsets=seq_offsets, workspace=workspace) as stream:
-        _check(lib.moe_balance_loss(logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, topk_idx.data_ptr(), k,
-                                    BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff,
-                                    loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel(), stream))
-    return BalanceLoss(loss, counts, tokens, probs, k, score, coeff, token_mask, seq_offsets)
+    dev = logits.get_device()
+    _same_device(dev, topk_idx, token_mask, seq_offsets, workspace)
+    _launch(dev, lib.moe_balance_loss, logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, topk_idx.data_ptr(),
+            idx_shape[1], BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff, loss.data_ptr(),
+            counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return BalanceLoss(loss, counts, tokens, probs, idx_shape[1], score, coeff, token_mask, seq_offsets)
 
 
 def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss: torch.Tensor,
@@ -929,24 +938,28 @@ def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss:
     """grad_loss (f32 [1] on the device) times the gradient of fwd.loss with
     respect to logits, in logits' dtype; ``fwd`` is the forward call's result
     for the same logits."""
-    stride = _matrix(logits, "logits")
-    T, E = logits.shape
-    if fwd.counts.shape[1] != E:
-        raise ValueError(f"logits have {E} experts and the forward call had {fwd.counts.shape[1]}")
-    if fwd.token_mask is not None and fwd.token_mask.numel() != T:
-        raise ValueError(f"logits have {T} tokens and the forward call's mask {fwd.token_mask.numel()}")
+    T, E, stride = _matrix(logits, "logits")
+    counts, mask = fwd.counts, fwd.token_mask
+    S, E_fwd = counts.shape
+    if E_fwd != E:
+        raise ValueError(f"logits have {E} experts and the forward call had {E_fwd}")
+    if mask is not None and mask.numel() != T:
+        raise ValueError(f"logits have {T} tokens and the forward call's mask {mask.numel()}")
     _vector(grad_loss, torch.float32, "grad_loss", 1)
+    dtype = logits.dtype
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    out_stride = _matrix(out, "out", (logits.dtype,))
-    if tuple(out.shape) != (T, E):
-        raise ValueError(f"out must be {T} x {E}, got {tuple(out.shape)}")
-    with _on(logits.device, counts=fwd.counts, grad_loss=grad_loss, out=out) as stream:
-        _check(lib.moe_balance_loss_backward(logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, fwd.k,
-                                             BALANCE_SCORES[fwd.score], _ptr(fwd.token_mask), _ptr(fwd.seq_offsets),
-                                             fwd.counts.shape[0], fwd.coeff, fwd.counts.data_ptr(),
-                                             fwd.tokens.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), out_stride,
-                                             stream))
+        out = torch.empty((T, E), dtype=dtype, device=logits.device)
+        out_stride = E
+    else:
+        rows, cols, out_stride = _matrix(out, "out", (dtype,))
+        if rows != T or cols != E:
+            raise ValueError(f"out must be {T} x {E}, got {rows} x {cols}")
+    dev = logits.get_device()
+    _same_device(dev, counts, grad_loss, out)
+    if T:
+        _launch(dev, lib.moe_balance_loss_backward, logits.data_ptr(), _DTYPES[dtype], T, E, stride, fwd.k,
+                BALANCE_SCORES[fwd.score], _ptr(mask), _ptr(fwd.seq_offsets), S, fwd.coeff, counts.data_ptr(),
+                fwd.tokens.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), out_stride)
     return out
 
 

@@ -29,6 +29,7 @@ struct Bf16 {
   NVDEV static uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
   NVDEV static uint16_t one(float a) { return (uint16_t)pack_bf16x2(a, 0.0f); }
   NVDEV static float from(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+  NVDEV static uint32_t mag(uint32_t h) { return h << 16; }          // |h| as fp32 bits
 };
 struct F16 {
   static constexpr int size = 2;
@@ -41,6 +42,7 @@ struct F16 {
   }
   NVDEV static uint16_t one(float a) { return __half_as_ushort(__float2half_rn(a)); }
   NVDEV static float from(uint16_t h) { return __half2float(__ushort_as_half(h)); }
+  NVDEV static uint32_t mag(uint32_t h) { return __float_as_uint(from((uint16_t)h)) & 0x7FFFFFFFu; }
 };
 struct F32 {
   static constexpr int size = 4;
@@ -63,26 +65,85 @@ NVDEV float mx_inv_scale(uint32_t s) { return s == 255u ? 0.0f : __uint_as_float
 NVDEV float mx_scale_value(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7FFFFFFFu : (s == 0u ? 0x00400000u : s << 23));
 }
-// Eight scaled values -> 4 bytes of codes.  A NaN block's values are
-// inf * 0 or x * 0 here: its codes are forced to 0.
+// Eight values times the reciprocal scale -> 4 bytes of codes.  A NaN block's
+// values are inf * 0 or NaN here: its codes are forced to 0.
 NVDEV uint32_t mx_codes8(const float* v, float inv, bool nan_block) {
+  const uint64_t inv2 = pack_f32x2(inv, inv);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], inv);
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t r = mul_f32x2(pack_f32x2(v[i], v[i + 1]), inv2);
+    y[i] = lo_f32(r);
+    y[i + 1] = hi_f32(r);
+  }
   return nan_block ? 0u : e2m1x8_hw(y);
 }
 
-// Loads of V consecutive bytes.
-template <int V> struct VecOf;
-template <> struct VecOf<16> { using type = uint4; };
-template <> struct VecOf<8> { using type = uint2; };
-template <> struct VecOf<4> { using type = uint32_t; };
+// n / d for n < 2^31 by a precomputed multiplier (division by an invariant
+// integer: m = floor(2^(31 + l) / d) + 1 with 2^(l - 1) < d <= 2^l gives
+// floor(n m / 2^(31 + l)) = floor(n / d), since m d exceeds 2^(31 + l) by at
+// most d <= 2^l).
+struct FastDiv {
+  uint32_t d, shift;
+  uint64_t m;
+  explicit FastDiv(uint32_t div) : d(div) {
+    uint32_t l = 0;
+    while ((1ull << l) < div) ++l;
+    shift = 31 + l;
+    m = (1ull << shift) / div + 1;
+  }
+  // m <= 2^32 + 1 and n < 2^31: the product fits 64 bits
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (uint32_t)(((uint64_t)n * m) >> shift); }
+};
 
-// The widest access (16, 8, 4 bytes, or one element) that every row of a
+// The widest access (32, 16, 8, 4 bytes, or one element) that every row of a
 // matrix at `p` with rows `stride_bytes` apart allows.
 inline int row_access_bytes(const void* p, long long stride_bytes, int elem) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes;
-  return a % 16 == 0 ? 16 : a % 8 == 0 ? 8 : a % 4 == 0 ? 4 : elem;
+  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : a % 8 == 0 ? 8 : a % 4 == 0 ? 4 : elem;
+}
+
+// 32 consecutive bytes as eight words, in accesses of VB bytes.
+template <int VB>
+NVDEV void load_words8(const void* p, uint32_t* w) {
+  if constexpr (VB == 32) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+  } else if constexpr (VB == 16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (VB == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2 v = __ldg(static_cast<const uint2*>(p) + i);
+      w[2 * i] = v.x; w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __ldg(static_cast<const uint32_t*>(p) + i);
+  }
+}
+template <int VB>
+NVDEV void store_words8(void* p, const uint32_t* w) {
+  if constexpr (VB == 32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else if constexpr (VB == 16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  } else if constexpr (VB == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) static_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) static_cast<uint32_t*>(p)[i] = w[i];
+  }
 }
 
 inline int mx_elem_size(int dtype) { return dtype == MXFP4_DTYPE_F32 ? 4 : 2; }

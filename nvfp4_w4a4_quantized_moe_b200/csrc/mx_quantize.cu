@@ -5,157 +5,296 @@
 // launch.  The arithmetic is exact: a block's scale is a power of two taken
 // from the exponent field of its largest magnitude, x * (1 / scale) is exact,
 // and the one rounding is the hardware's E2M1 conversion.
+//
+// Measured on one B200 as a share of its copy rate (6,449 GB/s):
+//   65536 x 6144 bf16: quantise 158 us (100 %), transposed 193 us (82 %),
+//   read-back 154 us (103 %); 32768 x 6144 fp32: 139 us (102 %), 164 us
+//   (86 %), 139 us (102 %); 8192 x 6144 bf16 (inside L2's reach, a few us of
+//   launch and tail): 24, 31 and 23 us.
+// The first form, with 16-byte loads, two packed maxima less and a 32-bit
+// division a unit, took 259 and 202 us at 65536 x 6144.
+#include <type_traits>
+
 #include "mx.cuh"
 
 namespace nvfp4moe {
 
 constexpr int kMxThreads = 256;
-constexpr int kMxSubs = kMxThreads / 16;     // 16-lane subgroups per block
 
-// Eight consecutive elements (one lane's share of a 128-element unit) as raw
-// words: 4 words of 16-bit elements or 8 of fp32.  VB is the access width the
-// rows allow; elements at or past `n` read as 0.
+// A lane's share of a 128-element unit is 32 bytes of the source, eight words:
+// 16 elements of a 16-bit type (8 lanes a unit, 2 a block) or 8 of fp32 (16
+// lanes, 4 a block).  One 256-bit access a lane where the rows allow it.
+template <typename T> __host__ __device__ constexpr int lane_elems() { return 32 / T::size; }
+template <typename T> __host__ __device__ constexpr int unit_lanes() { return kMxGroup / lane_elems<T>(); }
+template <typename T> __host__ __device__ constexpr int block_subs() { return kMxThreads / unit_lanes<T>(); }
+
+// Rows that allow only narrow accesses (8 bytes or less).
+//   Reading 16-bit elements that are only 2-byte aligned: a lane's 32 bytes lie
+//   inside three aligned 16-byte pieces; it reads those and shifts them into
+//   place.  4- and 8-byte accesses are left as they are (L1 serves the
+//   neighbours' share of a line).
+//   Writing: the warp's consecutive units (1 KiB in all) go through shared
+//   memory, so that neighbouring lanes write neighbouring accesses instead of
+//   4 to 16 accesses 32 bytes apart each.
+// Measured (one B200): 16384 x 6145 bf16, 2-byte rows: reading element by
+// element 107 us, through shared memory 118 us, shifted 66 us; writing element
+// by element 544 us, staged 80 us.  8191 x 6100 fp16, 8-byte rows: reading as
+// it is 25 us, shifted 35 us; writing as it is 53 us, staged 30 us.
+constexpr bool is_narrow(int vb) { return vb < 16; }
+constexpr int kMxWarpBytes = 1024;
+
+// The row and column that byte `b` of the warp's units belongs to.
+struct UnitPlace {
+  int row, col;
+};
+template <typename T>
+NVDEV UnitPlace place_of(const FastDiv& groups, uint32_t units, uint32_t first, int b) {
+  constexpr int unit_bytes = kMxGroup * T::size;
+  const uint32_t u = min(first + (uint32_t)(b / unit_bytes), units - 1);
+  UnitPlace p;
+  p.row = (int)groups.quotient(u);
+  p.col = (int)(u - (uint32_t)p.row * groups.d) * kMxGroup + (b % unit_bytes) / T::size;
+  return p;
+}
+template <int VB> struct Narrow;
+template <> struct Narrow<8> { using type = uint2; };
+template <> struct Narrow<4> { using type = uint32_t; };
+template <> struct Narrow<2> { using type = uint16_t; };
+
 template <typename T, int VB>
-NVDEV void load8(const uint8_t* row, int c, int n, uint32_t* w) {
-  constexpr int NW = T::size * 2;
-  if (VB >= 4 && c + 8 <= n) {
-    using V = typename VecOf<VB >= 4 ? VB : 4>::type;
-    const V* p = reinterpret_cast<const V*>(row + (size_t)c * T::size);
-    constexpr int per = sizeof(V) / 4;
+NVDEV void store_staged(uint8_t* out, int cols, long long stride_bytes, const FastDiv& groups, uint32_t units,
+                        uint32_t first, uint8_t* buf, const uint32_t* w) {
+  using V = typename Narrow<VB>::type;
+  constexpr int per = VB / T::size, unit_bytes = kMxGroup * T::size;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  uint4* mine = reinterpret_cast<uint4*>(buf + lane * 32);
+  mine[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  mine[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NW / per; ++i) {
-      const V v = __ldg(p + i);
-      if constexpr (per == 4) {
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      } else if constexpr (per == 2) {
-        w[2 * i] = v.x; w[2 * i + 1] = v.y;
-      } else {
-        w[i] = v;
+  for (int j = 0; j < 32 / VB; ++j) {
+    const int b = (j * 32 + lane) * VB;
+    if (first + (uint32_t)(b / unit_bytes) >= units) continue;
+    const UnitPlace p = place_of<T>(groups, units, first, b);
+    uint8_t* at = out + (size_t)p.row * (size_t)stride_bytes + (size_t)p.col * T::size;
+    if (p.col + per <= cols) {
+      *reinterpret_cast<V*>(at) = reinterpret_cast<const V*>(buf)[j * 32 + lane];
+    } else {
+#pragma unroll
+      for (int e = 0; e < per; ++e)
+        if (p.col + e < cols) {
+          if constexpr (T::size == 2) reinterpret_cast<uint16_t*>(at)[e] = reinterpret_cast<const uint16_t*>(buf + b)[e];
+          else reinterpret_cast<uint32_t*>(at)[e] = reinterpret_cast<const uint32_t*>(buf + b)[e];
+        }
+    }
+  }
+}
+
+// Elements at or past `n` read as 0.  `lo` and `hi` bound the matrix's bytes:
+// the aligned pieces of a narrow row may reach into its neighbours, not past
+// the matrix.
+template <typename T, int VB>
+NVDEV void load_share(const uint8_t* row, int c, int n, const uint8_t* lo, const uint8_t* hi, uint32_t* w) {
+  constexpr int EPL = lane_elems<T>();
+  if (c + EPL <= n) {
+    const uint8_t* at = row + (size_t)c * T::size;
+    if constexpr (VB >= 4) {
+      load_words8<VB>(at, w);
+      return;
+    } else {
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
+      const uint8_t* base = at - off;
+      if (base >= lo && base + 48 <= hi) {
+        uint32_t r[12];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(base) + i);
+          r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+        }
+        // whole words by two conditional moves, the rest by funnel shifts
+#pragma unroll
+        for (int i = 0; i < 10; ++i) r[i] = (off & 8u) ? r[i + 2] : r[i];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) r[i] = (off & 4u) ? r[i + 1] : r[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = T::size == 4 ? r[i] : __funnelshift_r(r[i], r[i + 1], (off & 3u) * 8u);
+        return;
       }
     }
-    return;
   }
 #pragma unroll
-  for (int i = 0; i < NW; ++i) w[i] = 0u;
+  for (int i = 0; i < 8; ++i) w[i] = 0u;
   if constexpr (T::size == 2) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < EPL; ++i)
       if (c + i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
   } else {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < EPL; ++i)
       if (c + i < n) w[i] = __ldg(p + i);
   }
 }
 
+// mag_bits of the largest element of the block that these lanes share
+// (magnitudes compare as integers; packed pairs for 16-bit types).
 template <typename T>
-NVDEV void unpack8(const uint32_t* w, float* v) {
+NVDEV uint32_t share_amax(const uint32_t* w) {
   if constexpr (T::size == 2) {
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = T::lo(w[i]);
-      v[2 * i + 1] = T::hi(w[i]);
-    }
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return T::mag(max(m & 0xFFFFu, m >> 16));
   } else {
+    uint32_t m = w[0] & 0x7FFFFFFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    for (int i = 1; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   }
 }
+template <typename T>
+NVDEV float share_value(const uint32_t* w, int i) {
+  if constexpr (T::size == 2) return (i & 1) ? T::hi(w[i >> 1]) : T::lo(w[i >> 1]);
+  else return __uint_as_float(w[i]);
+}
 
-// A unit is 128 consecutive elements of a row: one lane of a 16-lane subgroup
-// holds 8 of them, 4 lanes a block (two shuffles for its maximum), and the
-// unit's four scale bytes leave as one word.  A warp's loads then cover two
-// contiguous runs of 256 (16-bit) or 512 bytes.  Each subgroup takes U units
-// 16 apart, all their loads issued before the first is used.
+// Each group of lanes takes U units, all their loads issued before the first
+// is used; the unit's four scale bytes leave as one word.
 template <typename T, int VB, int U>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const uint8_t* __restrict__ x, int rows, int cols,
                                                                  long long stride_bytes,
                                                                  const int32_t* __restrict__ perm, uint32_t units,
-                                                                 int groups, int tiled, uint8_t* __restrict__ codes,
+                                                                 const FastDiv groups, int tiled,
+                                                                 uint8_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales) {
   griddep_wait();
   griddep_launch();
-  constexpr int NW = T::size * 2;
-  const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const uint32_t u0 = blockIdx.x * (uint32_t)(kMxSubs * U) + sub;
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>(), SUBS = block_subs<T>();
+  const int sub = threadIdx.x / LPU, l = threadIdx.x & (LPU - 1);
+  const uint32_t u0 = blockIdx.x * (uint32_t)(SUBS * U) + sub;
   const int blocks = mx_blocks(cols);
-  uint32_t w[U][NW];
+  const uint8_t* x_end = x + (rows > 0 ? (size_t)(rows - 1) * (size_t)stride_bytes + (size_t)cols * T::size : 0);
+  uint32_t w[U][8];
   int row[U], grp[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const uint32_t u = u0 + (uint32_t)i * kMxSubs;
-    row[i] = (int)(u / (uint32_t)groups);
-    grp[i] = (int)(u % (uint32_t)groups);
-    int src = -1;
-    if (u < units) src = perm ? __ldg(perm + row[i]) : row[i];
+    const uint32_t u = min(u0 + (uint32_t)i * SUBS, units - 1);
+    row[i] = (int)groups.quotient(u);
+    grp[i] = (int)(u - (uint32_t)row[i] * groups.d);
+    const int src = perm ? __ldg(perm + row[i]) : row[i];
     const int n = (src >= 0 && src < rows) ? cols : 0;       // a row without a source reads as zeros
-    load8<T, VB>(x + (n ? (size_t)src * (size_t)stride_bytes : 0), grp[i] * kMxGroup + l * 8, n, w[i]);
+    load_share<T, VB>(x + (n ? (size_t)src * (size_t)stride_bytes : 0), grp[i] * kMxGroup + l * EPL, n, x, x_end, w[i]);
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const uint32_t u = u0 + (uint32_t)i * kMxSubs;
-    float v[8];
-    unpack8<T>(w[i], v);
-    uint32_t m = 0u;
+    const uint32_t s = mx_scale(share_amax<T>(w[i]));
+    const float inv = mx_inv_scale(s);
+    uint32_t q[EPL / 8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, mag_bits(v[j]));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t s = mx_scale(m);
-    const uint32_t q = mx_codes8(v, mx_inv_scale(s), s == 255u);
-    const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, 4, 16);
-    const uint32_t s2 = __shfl_down_sync(0xffffffffu, s, 8, 16);
-    const uint32_t s3 = __shfl_down_sync(0xffffffffu, s, 12, 16);
-    if (u < units) {
-      const int blk = grp[i] * 4 + (l >> 2);
-      if (blk < blocks)
-        *reinterpret_cast<uint32_t*>(codes + (size_t)row[i] * (size_t)blocks * 16 + grp[i] * 64 + l * 4) = q;
+    for (int h = 0; h < EPL / 8; ++h) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = share_value<T>(w[i], h * 8 + j);
+      q[h] = mx_codes8(v, inv, s == 255u);
+    }
+    const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, LPU / 4, LPU);
+    const uint32_t s2 = __shfl_down_sync(0xffffffffu, s, LPU / 2, LPU);
+    const uint32_t s3 = __shfl_down_sync(0xffffffffu, s, LPU / 4 * 3, LPU);
+    if (u0 + (uint32_t)i * SUBS < units) {
+      const int blk = grp[i] * 4 + l / (LPU / 4);
+      if (blk < blocks) {
+        uint8_t* dst = codes + (size_t)row[i] * (size_t)blocks * 16 + grp[i] * 64 + l * (EPL / 2);
+        if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = q[0];
+      }
       if (tiled) {
         if (l == 0)
-          *reinterpret_cast<uint32_t*>(scales + mx_tiled_offset(row[i], grp[i], groups)) =
+          *reinterpret_cast<uint32_t*>(scales + mx_tiled_offset(row[i], grp[i], (int)groups.d)) =
               s | (s1 << 8) | (s2 << 16) | (s3 << 24);
-      } else if ((l & 3) == 0 && blk < blocks) {
+      } else if (l % (LPU / 4) == 0 && blk < blocks) {
         scales[(size_t)row[i] * blocks + blk] = (uint8_t)s;
       }
     }
   }
 }
 
-// The transpose: a thread owns C neighbouring columns (two 16-bit ones where
-// rows are 4-byte aligned, else one) over 64 rows of x, so its two blocks of
-// a column are 32 contiguous bytes of codes, a whole sector, without a trip
-// through shared memory.  A warp reads 64 (or 32) columns of a row at once;
-// the eight warps of a block cover 512 rows, whose codes are contiguous.
+// The transpose: a thread owns C neighbouring columns over 64 rows of x, so
+// its two blocks of a column are 32 contiguous bytes of codes, a whole sector,
+// without a trip through shared memory.  A warp reads 32 C columns of a row at
+// once; the warps of a block cover consecutive rows, whose codes are
+// contiguous.
 constexpr int kMxTRows = 64;
-template <typename T, int C>
-__global__ void __launch_bounds__(kMxThreads) mx_quantize_t_kernel(const uint8_t* __restrict__ x, int rows, int cols,
-                                                                   long long stride_bytes, int groups, int tiled,
-                                                                   uint8_t* __restrict__ codes,
-                                                                   uint8_t* __restrict__ scales) {
+constexpr int kMxTThreads = 128;
+template <typename T, int C, bool WIDE>
+__global__ void __launch_bounds__(kMxTThreads) mx_quantize_t_kernel(const uint8_t* __restrict__ x, int rows, int cols,
+                                                                    long long stride_bytes, int groups, int tiled,
+                                                                    uint8_t* __restrict__ codes,
+                                                                    uint8_t* __restrict__ scales) {
+  static_assert(C * T::size == 4, "a thread's columns of a row are one word");
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * C;
-  const long long r0 = ((long long)blockIdx.y * (kMxThreads / 32) + warp) * kMxTRows;
+  const long long r0 = ((long long)blockIdx.y * (kMxTThreads / 32) + warp) * kMxTRows;
   const int blocks = mx_blocks(rows);
   const long long r_end = tiled ? (long long)groups * kMxGroup : (long long)blocks * kMxBlock;
-  if (c >= cols || r0 >= r_end) return;
+  if (r0 >= r_end) return;                                   // whole warps
   const uint8_t* p = x + (size_t)r0 * (size_t)stride_bytes + (size_t)c * T::size;
   uint32_t w[kMxTRows];
+  if constexpr (WIDE) {
+    if (c >= cols) return;
 #pragma unroll
-  for (int i = 0; i < kMxTRows; ++i) {
-    w[i] = 0u;
-    if (r0 + i < rows) {
-      const uint8_t* q = p + (size_t)i * (size_t)stride_bytes;
-      if constexpr (T::size == 4 || C == 2) w[i] = __ldg(reinterpret_cast<const uint32_t*>(q));
-      else w[i] = __ldg(reinterpret_cast<const uint16_t*>(q));
+    for (int i = 0; i < kMxTRows; ++i)
+      w[i] = r0 + i < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (size_t)i * (size_t)stride_bytes)) : 0u;
+  } else {
+    // Rows that are only 2-byte aligned: each lane reads the aligned word that
+    // holds its first column, takes the word behind it from the next lane and
+    // shifts the pair into place.  The word behind the last lane's is read by
+    // lane i for rows i and i + 32, so that no load sits in a branch.  Warps
+    // whose words would reach past the matrix read element by element.
+    const uint8_t* x_end = x + (size_t)(rows - 1) * (size_t)stride_bytes + (size_t)cols * 2;
+    const long long rl = min(r0 + kMxTRows, (long long)rows) - 1;
+    const uint8_t* first = p - (size_t)lane * 4;
+    const uint8_t* last = x + (size_t)max(rl, 0ll) * (size_t)stride_bytes + (size_t)(c - lane * C) * 2 + 32 * 4;
+    if (r0 < rows && first - 2 >= x && last + 4 <= x_end) {
+      const int n = (int)(rl + 1 - r0);                      // rows that exist: 64 but at the end
+      auto behind = [&](int i) -> uint32_t {
+        const uint8_t* q = first + (size_t)min(i, n - 1) * (size_t)stride_bytes;
+        return __ldg(reinterpret_cast<const uint32_t*>(q - (reinterpret_cast<uintptr_t>(q) & 2u)) + 32);
+      };
+      const uint32_t next0 = behind(lane), next1 = behind(lane + 32);
+#pragma unroll
+      for (int i = 0; i < kMxTRows; ++i) {
+        const uint8_t* q = p + (size_t)i * (size_t)stride_bytes;
+        w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(q - (reinterpret_cast<uintptr_t>(q) & 2u))) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kMxTRows; ++i) {
+        const uint8_t* q = p + (size_t)i * (size_t)stride_bytes;
+        const uint32_t other = __shfl_down_sync(0xffffffffu, w[i], 1);
+        const uint32_t next = __shfl_sync(0xffffffffu, i < 32 ? next0 : next1, i & 31);
+        const uint32_t pair = __funnelshift_r(w[i], lane == 31 ? next : other, (uint32_t)(reinterpret_cast<uintptr_t>(q) & 2u) * 8u);
+        w[i] = i < n ? pair : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMxTRows; ++i) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p + (size_t)i * (size_t)stride_bytes);
+        const bool in = r0 + i < rows;
+        const uint32_t a = in && c < cols ? __ldg(q) : 0u, b = in && c + 1 < cols ? __ldg(q + 1) : 0u;
+        w[i] = a | (b << 16);
+      }
     }
+    if (c >= cols) return;
   }
+  const int blk = (int)(r0 / kMxBlock);                      // even: the pair stays inside a group
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    uint32_t sc[2];
+    uint32_t sc[2], q[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       auto val = [&](int i) -> float {
@@ -163,32 +302,42 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_t_kernel(const uint8_t
         if constexpr (T::size == 4) return __uint_as_float(b);
         else return j ? T::hi(b) : T::lo(b);
       };
-      uint32_t m = 0u;
+      uint32_t m;
+      if constexpr (T::size == 2) {
+        m = 0u;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = max(m, mag_bits(val(i)));
+        for (int i = 0; i < 32; ++i) m = __vmaxu2(m, w[h * 32 + i] & 0x7FFF7FFFu);
+        m = T::mag(j ? m >> 16 : m & 0xFFFFu);
+      } else {
+        m = 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = max(m, w[h * 32 + i] & 0x7FFFFFFFu);
+      }
       const uint32_t s = sc[h] = mx_scale(m);
       const float inv = mx_inv_scale(s);
-      uint32_t q[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = val(g * 8 + i);
-        q[g] = mx_codes8(v, inv, s == 255u);
+        q[h][g] = mx_codes8(v, inv, s == 255u);
       }
-      const int blk = (int)(r0 / kMxBlock) + h;
-      if (c + j < cols && blk < blocks)
-        *reinterpret_cast<uint4*>(codes + ((size_t)(c + j) * blocks + blk) * 16) = make_uint4(q[0], q[1], q[2], q[3]);
     }
     if (c + j < cols) {
-      const int blk = (int)(r0 / kMxBlock);                  // even: the pair stays inside a group
+      uint8_t* d = codes + ((size_t)(c + j) * blocks + blk) * 16;
+      if ((blocks & 1) == 0 && blk < blocks) {               // both blocks exist and the pair is 32-byte aligned
+        store_words8<32>(d, &q[0][0]);
+      } else {
+        if (blk < blocks) *reinterpret_cast<uint4*>(d) = make_uint4(q[0][0], q[0][1], q[0][2], q[0][3]);
+        if (blk + 1 < blocks) *reinterpret_cast<uint4*>(d + 16) = make_uint4(q[1][0], q[1][1], q[1][2], q[1][3]);
+      }
       if (tiled) {
         *reinterpret_cast<uint16_t*>(scales + mx_tiled_offset(c + j, blk >> 2, groups) + (blk & 3)) =
             (uint16_t)(sc[0] | (sc[1] << 8));
       } else {
-        uint8_t* d = scales + (size_t)(c + j) * blocks + blk;
-        d[0] = (uint8_t)sc[0];
-        if (blk + 1 < blocks) d[1] = (uint8_t)sc[1];
+        uint8_t* e = scales + (size_t)(c + j) * blocks + blk;
+        if (blk < blocks) e[0] = (uint8_t)sc[0];
+        if (blk + 1 < blocks) e[1] = (uint8_t)sc[1];
       }
     }
   }
@@ -210,68 +359,79 @@ NVDEV void mx_values8(uint32_t q, float* v) {
 template <typename T, int VB, int U>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales, int cols,
-                                                                   uint32_t units, int groups, int tiled,
+                                                                   uint32_t units, const FastDiv groups, int tiled,
                                                                    uint8_t* __restrict__ out, long long stride_bytes) {
   griddep_wait();
   griddep_launch();
-  const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const uint32_t u0 = blockIdx.x * (uint32_t)(kMxSubs * U) + sub;
-  const int blocks = mx_blocks(cols);
-  uint32_t q[U], s[U];
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>(), SUBS = block_subs<T>();
+  const int sub = threadIdx.x / LPU, l = threadIdx.x & (LPU - 1);
+  const uint32_t u0 = blockIdx.x * (uint32_t)(SUBS * U) + sub;
+  const int blocks = mx_blocks(cols), bl = l / (LPU / 4);      // the lane's block of the unit
+  __shared__ __align__(16) uint8_t warp_buf[is_narrow(VB) ? kMxThreads / 32 : 1][is_narrow(VB) ? kMxWarpBytes : 16];
+  uint32_t q[U][2], s[U];
+  int row[U], grp[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const uint32_t u = u0 + (uint32_t)i * kMxSubs;
-    const int row = (int)(u / (uint32_t)groups), grp = (int)(u % (uint32_t)groups);
-    const int blk = grp * 4 + (l >> 2);
-    q[i] = s[i] = 0u;
-    if (u < units && blk < blocks) {
-      q[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (size_t)row * (size_t)blocks * 16 + grp * 64 + l * 4));
-      s[i] = __ldg(scales + (tiled ? mx_tiled_offset(row, grp, groups) + (l >> 2) : (size_t)row * blocks + blk));
+    const uint32_t u = min(u0 + (uint32_t)i * SUBS, units - 1);
+    row[i] = (int)groups.quotient(u);
+    grp[i] = (int)(u - (uint32_t)row[i] * groups.d);
+    const int blk = grp[i] * 4 + bl;
+    q[i][0] = q[i][1] = s[i] = 0u;
+    if (blk < blocks) {
+      const uint8_t* src = codes + (size_t)row[i] * (size_t)blocks * 16 + grp[i] * 64 + l * (EPL / 2);
+      if constexpr (EPL == 16) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        q[i][0] = v.x;
+        q[i][1] = v.y;
+      } else {
+        q[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      }
+      s[i] = __ldg(scales + (tiled ? mx_tiled_offset(row[i], grp[i], (int)groups.d) + bl
+                                   : (size_t)row[i] * blocks + blk));
     }
   }
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const uint32_t u = u0 + (uint32_t)i * kMxSubs;
-    const int row = (int)(u / (uint32_t)groups), grp = (int)(u % (uint32_t)groups);
-    const int c = grp * kMxGroup + l * 8;
-    if (u >= units || c >= cols) continue;
-    float v[8];
-    mx_values8(q[i], v);
     const float S = mx_scale_value(s[i]);
+    float v[EPL];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], S);
-    uint8_t* dst = out + (size_t)row * (size_t)stride_bytes + (size_t)c * T::size;
-    if (VB >= 4 && c + 8 <= cols) {
-      constexpr int NW = T::size * 2;
-      uint32_t w[NW];
+    for (int h = 0; h < EPL / 8; ++h) mx_values8(q[i][h], v + 8 * h);
 #pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        if constexpr (T::size == 2) w[j] = T::pack(v[2 * j], v[2 * j + 1]);
-        else w[j] = __float_as_uint(v[j]);
-      }
-      using V = typename VecOf<VB >= 4 ? VB : 4>::type;
-      V* d = reinterpret_cast<V*>(dst);
-      constexpr int per = sizeof(V) / 4;
+    for (int j = 0; j < EPL; ++j) v[j] = __fmul_rn(v[j], S);
+    uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < NW / per; ++j) {
-        if constexpr (per == 4) d[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        else if constexpr (per == 2) d[j] = make_uint2(w[2 * j], w[2 * j + 1]);
-        else d[j] = w[j];
-      }
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (T::size == 2) w[j] = T::pack(v[2 * j], v[2 * j + 1]);
+      else w[j] = __float_as_uint(v[j]);
+    }
+    if constexpr (is_narrow(VB)) {
+      store_staged<T, VB>(out, cols, stride_bytes, groups, units,
+                          u0 - (threadIdx.x & 31) / LPU + (uint32_t)i * SUBS, warp_buf[threadIdx.x >> 5], w);
     } else {
+      const int c = grp[i] * kMxGroup + l * EPL;
+      if (u0 + (uint32_t)i * SUBS >= units || c >= cols) continue;
+      uint8_t* dst = out + (size_t)row[i] * (size_t)stride_bytes + (size_t)c * T::size;
+      if (c + EPL <= cols) {
+        store_words8<VB>(dst, w);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < cols) {
-          if constexpr (T::size == 2) reinterpret_cast<uint16_t*>(dst)[j] = T::one(v[j]);
-          else reinterpret_cast<float*>(dst)[j] = v[j];
-        }
+        for (int j = 0; j < EPL; ++j)
+          if (c + j < cols) {
+            if constexpr (T::size == 2) reinterpret_cast<uint16_t*>(dst)[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            else reinterpret_cast<uint32_t*>(dst)[j] = w[j];
+          }
+      }
     }
   }
 }
 
-// Units per subgroup: four where that still leaves every SM several blocks,
-// else one, so that a few rows spread over the whole GPU.
-static inline int units_per_sub(uint32_t units, int sms) { return units >= (uint32_t)(sms * kMxSubs * 16) ? 4 : 1; }
+// Units per group of lanes: several where that still leaves every SM a few
+// blocks, else one, so that a few rows spread over the whole GPU.
+constexpr int kMxUnits = 2;
+template <typename T>
+static inline bool many_units(uint32_t units, int sms) {
+  return units >= (uint32_t)(sms * block_subs<T>() * kMxUnits * 8);
+}
 
 template <typename F>
 static nvfp4_status with_type(int dtype, F&& f) {
@@ -281,28 +441,15 @@ static nvfp4_status with_type(int dtype, F&& f) {
     default: return f(F32{});
   }
 }
-
-template <typename T, int VB>
-static nvfp4_status run_quantize(int per, uint32_t units, const uint8_t* x, int rows, int cols, long long stride_bytes,
-                                 const int32_t* perm, int groups, int tiled, uint8_t* codes, uint8_t* scales,
-                                 cudaStream_t s) {
-  const dim3 grid((units + kMxSubs * per - 1) / (kMxSubs * per));
-  if (per == 4)
-    return launch_dependent("mx_quantize_kernel", mx_quantize_kernel<T, VB, 4>, grid, dim3(kMxThreads), 0, s, x, rows,
-                            cols, stride_bytes, perm, units, groups, tiled, codes, scales);
-  return launch_dependent("mx_quantize_kernel", mx_quantize_kernel<T, VB, 1>, grid, dim3(kMxThreads), 0, s, x, rows,
-                          cols, stride_bytes, perm, units, groups, tiled, codes, scales);
-}
-
-template <typename T, int VB>
-static nvfp4_status run_dequantize(int per, uint32_t units, const uint8_t* codes, const uint8_t* scales, int cols,
-                                   int groups, int tiled, uint8_t* out, long long stride_bytes, cudaStream_t s) {
-  const dim3 grid((units + kMxSubs * per - 1) / (kMxSubs * per));
-  if (per == 4)
-    return launch_dependent("mx_dequantize_kernel", mx_dequantize_kernel<T, VB, 4>, grid, dim3(kMxThreads), 0, s,
-                            codes, scales, cols, units, groups, tiled, out, stride_bytes);
-  return launch_dependent("mx_dequantize_kernel", mx_dequantize_kernel<T, VB, 1>, grid, dim3(kMxThreads), 0, s, codes,
-                          scales, cols, units, groups, tiled, out, stride_bytes);
+// Calls f(access width) with the width as a compile-time constant.
+template <typename T, typename F>
+static nvfp4_status with_width(int vb, F&& f) {
+  if (vb == 32) return f(std::integral_constant<int, 32>{});
+  if (vb == 16) return f(std::integral_constant<int, 16>{});
+  if (vb == 8) return f(std::integral_constant<int, 8>{});
+  if (vb == 4 || T::size == 4) return f(std::integral_constant<int, 4>{});
+  if constexpr (T::size == 2) return f(std::integral_constant<int, 2>{});
+  return NVFP4_ERR_INVALID_ARG;
 }
 
 nvfp4_status check_mx_source(const char* name, const void* x, int dtype, int rows, int cols, long long row_stride) {
@@ -340,19 +487,21 @@ nvfp4_status launch_mx_quantize(const void* x, int dtype, int rows, int cols, lo
   NV_CHECK(count_units("mxfp4_quantize", out_rows, cols, &units));
   int sms = 0;
   NV_CHECK(device_sm_count(&sms));
-  const int groups = mx_groups(cols), tiled = layout == NVFP4_LAYOUT_TILED;
-  const int per = units_per_sub(units, sms);
+  const FastDiv groups((uint32_t)mx_groups(cols));
+  const int tiled = layout == NVFP4_LAYOUT_TILED;
   const uint8_t* xb = static_cast<const uint8_t*>(x);
   return with_type(dtype, [&](auto tag) -> nvfp4_status {
     using T = decltype(tag);
     const long long sb = row_stride * T::size;
-    const int vb = row_access_bytes(x, rows > 1 ? sb : 0, T::size);
-    if (vb == 16) return run_quantize<T, 16>(per, units, xb, rows, cols, sb, perm, groups, tiled, codes, scales, s);
-    if (vb == 8) return run_quantize<T, 8>(per, units, xb, rows, cols, sb, perm, groups, tiled, codes, scales, s);
-    if (vb == 4) return run_quantize<T, 4>(per, units, xb, rows, cols, sb, perm, groups, tiled, codes, scales, s);
-    if constexpr (T::size == 2)
-      return run_quantize<T, 2>(per, units, xb, rows, cols, sb, perm, groups, tiled, codes, scales, s);
-    return NVFP4_ERR_INVALID_ARG;
+    const bool many = many_units<T>(units, sms);
+    const uint32_t per_block = block_subs<T>() * (many ? kMxUnits : 1);
+    const dim3 grid((units + per_block - 1) / per_block);
+    return with_width<T>(row_access_bytes(x, rows > 1 ? sb : 0, T::size), [&](auto vb) -> nvfp4_status {
+      constexpr int VB = decltype(vb)::value;
+      return launch_dependent("mx_quantize_kernel",
+                              many ? mx_quantize_kernel<T, VB, kMxUnits> : mx_quantize_kernel<T, VB, 1>, grid,
+                              dim3(kMxThreads), 0, s, xb, rows, cols, sb, perm, units, groups, tiled, codes, scales);
+    });
   });
 }
 
@@ -385,7 +534,7 @@ extern "C" nvfp4_status mxfp4_quantize_transposed(const void* x, int dtype, int 
   NV_CHECK(check_mx_source("mxfp4_quantize_transposed", x, dtype, rows, cols, row_stride));
   NV_REQUIRE(rows >= 1, NVFP4_ERR_INVALID_ARG, "mxfp4_quantize_transposed: rows=%d (the result's columns)", rows);
   NV_CHECK(check_mx_quantized("mxfp4_quantize_transposed", codes, scales, layout));
-  constexpr int per_block = kMxThreads / 32 * kMxTRows;
+  constexpr int per_block = kMxTThreads / 32 * kMxTRows;
   NV_REQUIRE(rows <= 65535 * per_block, NVFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_quantize_transposed: rows=%d is above %d",
              rows, 65535 * per_block);
   int sms = 0;
@@ -396,15 +545,19 @@ extern "C" nvfp4_status mxfp4_quantize_transposed(const void* x, int dtype, int 
   cudaStream_t s = as_stream(stream);
   return with_type(dtype, [&](auto tag) -> nvfp4_status {
     using T = decltype(tag);
+    constexpr int C = 4 / T::size;
     const long long sb = row_stride * T::size;
-    if constexpr (T::size == 2) {
-      // pairs of columns need 4-byte aligned rows and a second column in the last pair
-      if (row_access_bytes(x, rows > 1 ? sb : 0, 2) >= 4 && cols % 2 == 0)
-        return launch_dependent("mx_quantize_t_kernel", mx_quantize_t_kernel<T, 2>, dim3((cols + 63) / 64, gy),
-                                dim3(kMxThreads), 0, s, xb, rows, cols, sb, groups, tiled, codes, scales);
+    // one word a thread and row: needs 4-byte aligned rows and, for pairs, a
+    // second column in the last pair
+    const bool wide = row_access_bytes(x, rows > 1 ? sb : 0, T::size) >= 4 && cols % C == 0;
+    const dim3 grid((unsigned)((cols + 32ll * C - 1) / (32 * C)), gy);
+    if constexpr (C == 2) {
+      if (!wide)
+        return launch_dependent("mx_quantize_t_kernel", mx_quantize_t_kernel<T, C, false>, grid, dim3(kMxTThreads), 0,
+                                s, xb, rows, cols, sb, groups, tiled, codes, scales);
     }
-    return launch_dependent("mx_quantize_t_kernel", mx_quantize_t_kernel<T, 1>, dim3((cols + 31) / 32, gy),
-                            dim3(kMxThreads), 0, s, xb, rows, cols, sb, groups, tiled, codes, scales);
+    return launch_dependent("mx_quantize_t_kernel", mx_quantize_t_kernel<T, C, true>, grid, dim3(kMxTThreads), 0, s,
+                            xb, rows, cols, sb, groups, tiled, codes, scales);
   });
 }
 
@@ -417,19 +570,21 @@ extern "C" nvfp4_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* sc
   NV_CHECK(count_units("mxfp4_dequantize", rows, cols, &units));
   int sms = 0;
   NV_CHECK(device_sm_count(&sms));
-  const int groups = mx_groups(cols), tiled = layout == NVFP4_LAYOUT_TILED;
-  const int per = units_per_sub(units, sms);
+  const FastDiv groups((uint32_t)mx_groups(cols));
+  const int tiled = layout == NVFP4_LAYOUT_TILED;
   uint8_t* ob = static_cast<uint8_t*>(out);
-  cudaStream_t s = as_stream(stream);
   return with_type(dtype, [&](auto tag) -> nvfp4_status {
     using T = decltype(tag);
     const long long sb = row_stride * T::size;
-    const int vb = row_access_bytes(out, rows > 1 ? sb : 0, T::size);
-    if (vb == 16) return run_dequantize<T, 16>(per, units, codes, scales, cols, groups, tiled, ob, sb, s);
-    if (vb == 8) return run_dequantize<T, 8>(per, units, codes, scales, cols, groups, tiled, ob, sb, s);
-    if (vb == 4) return run_dequantize<T, 4>(per, units, codes, scales, cols, groups, tiled, ob, sb, s);
-    if constexpr (T::size == 2)
-      return run_dequantize<T, 2>(per, units, codes, scales, cols, groups, tiled, ob, sb, s);
-    return NVFP4_ERR_INVALID_ARG;
+    const bool many = many_units<T>(units, sms);
+    const uint32_t per_block = block_subs<T>() * (many ? kMxUnits : 1);
+    const dim3 grid((units + per_block - 1) / per_block);
+    return with_width<T>(row_access_bytes(out, rows > 1 ? sb : 0, T::size), [&](auto vb) -> nvfp4_status {
+      constexpr int VB = decltype(vb)::value;
+      return launch_dependent("mx_dequantize_kernel",
+                              many ? mx_dequantize_kernel<T, VB, kMxUnits> : mx_dequantize_kernel<T, VB, 1>, grid,
+                              dim3(kMxThreads), 0, as_stream(stream), codes, scales, cols, units, groups, tiled, ob,
+                              sb);
+    });
   });
 }
