@@ -94,6 +94,13 @@ NVFP4_API nvfp4_status nvfp4_test_sigmoid(const float* l, int n, float* out, voi
  * Returns -1 when T < 1 or H is not a positive multiple of 64. */
 NVFP4_API int nvfp4_test_router_splits(int T, int H, int* stages_per_split);
 
+/* Host arithmetic only, no CUDA call: the tokens per tile of an MXFP4 product
+ * (mxfp4_matmul with these sizes on 148 SMs), with the K splits in *splits, 1
+ * or 0 in *pair for tiles on CTA pairs, and the pipeline stages in *stages
+ * (each nullable).  The order of the fp32 sums follows the splits.  Returns -1
+ * for M < 1, N < 1, K < 1 or E < 0. */
+NVFP4_API int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages);
+
 #ifdef __cplusplus
 }
 #endif

@@ -123,6 +123,8 @@ _declare("nvfp4_test_mma_peak", _i, _i, _i, _i, _i, _vp, _vp, _vp)
 _declare("nvfp4_test_wait_timeout", _i, _vp, ctypes.c_uint64, _vp, _sz, _vp, _vp, _vp)
 _declare("nvfp4_test_block_scale_div", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp)
 _declare("nvfp4_test_router_splits", _i, _i, _i, ctypes.POINTER(ctypes.c_int))
+_declare("nvfp4_test_mxfp4_plan", _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
+         ctypes.POINTER(ctypes.c_int))
 
 # Every symbol the public headers declare (checked by the CPU test suite).
 EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
@@ -140,7 +142,7 @@ EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "nvfp4_test_e2m1", "nvfp4_test_e2m1_sweep", "nvfp4_test_e4m3", "nvfp4_test_sigmoid",
            "nvfp4_test_mma_peak", "nvfp4_test_wait_timeout", "nvfp4_test_block_scale_div",
-           "nvfp4_test_router_splits")
+           "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan")
 
 
 def _check(status: int):
@@ -1001,6 +1003,15 @@ def nvfp4_test_router_splits(T: int, H: int):
     if n < 0:
         raise ValueError(f"no router split for T={T} H={H}")
     return n, per.value
+
+
+def nvfp4_test_mxfp4_plan(M: int, N: int, K: int, E: int = 0):
+    """(tokens per tile, K splits, on CTA pairs, pipeline stages) of an MXFP4 product."""
+    v = [ctypes.c_int(0) for _ in range(3)]
+    nt = lib.nvfp4_test_mxfp4_plan(M, N, K, E, *(ctypes.byref(x) for x in v))
+    if nt < 0:
+        raise ValueError(f"no MXFP4 product has M={M} N={N} K={K} E={E}")
+    return nt, v[0].value, bool(v[1].value), v[2].value
 
 
 def nvfp4_test_sigmoid(l: torch.Tensor):

@@ -25,13 +25,14 @@
 // second kernel and no workspace.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "mx.cuh"
+#include "../../include/nvfp4_moe_testing.h"
 
 namespace nvfp4moe {
 
 constexpr int kXBM = 128;                        // b rows per tile
-constexpr int kXMaxNT = 256;                     // tokens per tile, at most
 constexpr int kXBK = 256;                        // K elements per stage
 constexpr int kXRowBytes = kXBK / 2;             // 128 bytes of codes per row and stage
 constexpr int kXWBytes = kXBM * kXRowBytes;      // 16 KiB
@@ -41,10 +42,11 @@ constexpr int kXThreads = 320;
 constexpr int kXEpiWarps = 8;
 constexpr int kXMaxStages = 8;
 constexpr int kXMaxE = 1024;
+constexpr int kXMaxSplits = 8;                   // the largest portable cluster
 // Dynamic shared memory of a CTA that has an SM to itself, and of one of two
-// on an SM (228 KiB less 1 KiB a CTA; the static part is below 4.5 KiB).
-constexpr int kXMaxSmem = 227 * 1024 - 4608;
-constexpr int kXSmemPair = 228 * 1024 / 2 - 1024 - 4608;
+// on an SM (228 KiB less 1 KiB a CTA; the static part is below 256 bytes).
+constexpr int kXMaxSmem = 227 * 1024 - 256;
+constexpr int kXSmemPair = 228 * 1024 / 2 - 1024 - 256;
 
 struct MxGemmParams {
   int M, N, E;               // E = 0: dense
@@ -54,6 +56,8 @@ struct MxGemmParams {
   int nt;                    // tokens per tile
   int stages;
   int splits;                // K splits (CTAs per cluster)
+  int pairs;                 // 16-bit y whose rows are 4-byte aligned
+  int quads;                 // y whose rows are aligned to four elements
   int early_b;               // b is not written by the previous kernel of this call: load before the wait
   const int32_t* expert_offsets;
   const int32_t* expert_counts;
@@ -88,9 +92,12 @@ NVDEV void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t 
           d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem));
 }
-NVDEV float ld_shared_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+NVDEV float4 ld_shared_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -100,43 +107,53 @@ struct MxTile {
   int e, row0, tokens, wt;
 };
 
-// First tile group (128.. tokens of one expert) of every expert, as an
-// exclusive prefix in start[0..E], from device-side offsets that are not
-// trusted: a segment is clamped to [0, M] and its tokens to the segment.
-struct MxSegment {
-  int row0, tokens;
+// Grouped products: every expert's first tile group (`nt` tokens of one
+// expert), first row and tokens, in shared memory behind the stages.  The
+// device-side offsets are not trusted: a segment is clamped to [0, M] and its
+// tokens to the segment.
+struct MxSegments {
+  int *start, *row0, *tokens;      // [E + 1], [E], [E]
 };
-NVDEV MxSegment mx_segment(const MxGemmParams& p, int e) {
-  MxSegment g;
-  const int lo = min(max(p.expert_offsets[e], 0), p.M);
-  const int hi = min(max(p.expert_offsets[e + 1], lo), p.M);
-  g.row0 = lo & ~127;                            // a multiple of 128 by contract; never past the scale tiles
-  int n = hi - g.row0;
-  if (p.expert_counts) n = min(n, max(p.expert_counts[e], 0));
-  g.tokens = n;
-  return g;
-}
-NVDEV void mx_scan_segments(const MxGemmParams& p, int* start) {
+__host__ __device__ constexpr int mx_segment_bytes(int E) { return E ? (3 * E + 1) * 4 : 0; }
+NVDEV MxSegments mx_scan_segments(const MxGemmParams& p, uint8_t* at) {
+  MxSegments g;
+  g.start = reinterpret_cast<int*>(at);
+  g.row0 = g.start + p.E + 1;
+  g.tokens = g.row0 + p.E;
+  if (p.E == 0) return g;
   if ((threadIdx.x >> 5) == 0) {
     const int lane = threadIdx.x & 31;
     int carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int v = 0;
-      if (e < p.E) v = (mx_segment(p, e).tokens + p.nt - 1) / p.nt;
+      if (e < p.E) {
+        const int lo = min(max(p.expert_offsets[e], 0), p.M);
+        const int hi = min(max(p.expert_offsets[e + 1], lo), p.M);
+        const int r = lo & ~127;                 // a multiple of 128 by contract; never past the scale tiles
+        int n = hi - r;
+        if (p.expert_counts) n = min(n, max(p.expert_counts[e], 0));
+        g.row0[e] = r;
+        g.tokens[e] = n;
+        v = (n + p.nt - 1) / p.nt;
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
       }
-      if (e < p.E) start[e + 1] = carry + v;
+      if (e < p.E) g.start[e + 1] = carry + v;
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) start[0] = 0;
+    if (lane == 0) g.start[0] = 0;
   }
   __syncthreads();
+  return g;
 }
-NVDEV MxTile mx_tile(const MxGemmParams& p, const int* start, int t) {
+NVDEV int mx_num_tiles(const MxGemmParams& p, const MxSegments& g) {
+  return (p.E == 0 ? p.n_tt : g.start[p.E]) * p.n_wt;
+}
+NVDEV MxTile mx_tile(const MxGemmParams& p, const MxSegments& s, int t) {
   MxTile c;
   c.wt = t % p.n_wt;
   const int g = t / p.n_wt;
@@ -149,13 +166,12 @@ NVDEV MxTile mx_tile(const MxGemmParams& p, const int* start, int t) {
   int lo = 0, hi = p.E - 1;                      // the last expert whose tiles start at or before g
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= g) lo = mid; else hi = mid - 1;
+    if (s.start[mid] <= g) lo = mid; else hi = mid - 1;
   }
-  const MxSegment s = mx_segment(p, lo);
-  const int j = g - start[lo];
+  const int j = g - s.start[lo];
   c.e = lo;
-  c.row0 = s.row0 + j * p.nt;
-  c.tokens = min(p.nt, s.tokens - j * p.nt);
+  c.row0 = s.row0[lo] + j * p.nt;
+  c.tokens = min(p.nt, s.tokens[lo] - j * p.nt);
   return c;
 }
 
@@ -165,7 +181,58 @@ NVDEV void mx_store(void* y, size_t i, float v) {
   else static_cast<float*>(y)[i] = v;
 }
 
-template <typename T>
+// bias and row weight of one accumulator value (token m, the thread's column).
+template <bool PLAIN>
+NVDEV float mx_value(const MxGemmParams& p, uint32_t acc, int m, bool real, float bias) {
+  const float v = __uint_as_float(acc);
+  if constexpr (PLAIN) return v;
+  const float s = __fadd_rn(v, bias);
+  return p.row_weight ? __fmul_rn(s, real ? __ldg(p.row_weight + m) : 0.0f) : s;
+}
+
+// 16-bit outputs of two neighbouring tokens m, m + 1 of the thread's column n,
+// packed in one word (m in the low half).  The lanes of the warp hold 32
+// neighbouring n: lanes trade halves with their neighbour, so that each stores
+// two neighbouring outputs of one token (even lanes m, odd lanes m + 1) where
+// rows of y are 4-byte aligned.  `left`: real tokens from m on.
+NVDEV void mx_store_pair(const MxGemmParams& p, uint32_t word, uint16_t* at, int left, int n) {
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, word, 1);
+  const bool odd = n & 1;
+  const uint32_t v = __byte_perm(word, got, odd ? 0x3276 : 0x5410);
+  if (left > (odd ? 1 : 0)) {
+    if ((n | 1) < p.N) *reinterpret_cast<uint32_t*>(at) = v;
+    else if ((n & ~1) < p.N) *at = (uint16_t)v;              // y's last column is an even one
+  }
+}
+
+// A thread's 32 accumulator columns (tokens m0 ..., the first `cnt` real) of
+// output column n.
+template <typename T, bool PLAIN>
+NVDEV void mx_store32(const MxGemmParams& p, const uint32_t* r, int m0, int cnt, int n, float bias) {
+  if constexpr (T::size == 2) {
+    if (p.pairs) {
+      uint16_t* at = static_cast<uint16_t*>(p.y) + (size_t)(m0 + (n & 1)) * (size_t)p.y_stride + (n & ~1);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        mx_store_pair(p, T::pack(mx_value<PLAIN>(p, r[i], m0 + i, i < cnt, bias),
+                                 mx_value<PLAIN>(p, r[i + 1], m0 + i + 1, i + 1 < cnt, bias)),
+                      at, cnt - i, n);
+        at += 2 * (size_t)p.y_stride;
+      }
+      return;
+    }
+  }
+  if (n >= p.N) return;
+  size_t at = (size_t)m0 * (size_t)p.y_stride + n;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (i < cnt) mx_store<T>(p.y, at, mx_value<PLAIN>(p, r[i], m0 + i, true, bias));
+    at += (size_t)p.y_stride;
+  }
+}
+
+// PLAIN: neither bias nor row weight.
+template <typename T, bool PLAIN>
 __global__ void __launch_bounds__(kXThreads, 2)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmX32, const MxGemmParams p) {
@@ -173,16 +240,18 @@ __global__ void __launch_bounds__(kXThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kXMaxStages];
   __shared__ __align__(8) uint64_t empty_bar[kXMaxStages];
-  __shared__ __align__(8) uint64_t acc_full_bar;
-  __shared__ __align__(8) uint64_t acc_empty_bar;
+  __shared__ __align__(8) uint64_t acc_full_bar[2];
+  __shared__ __align__(8) uint64_t acc_empty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
-  __shared__ int seg_start[kXMaxE + 1];
   volatile int* abort_flag = &abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nt_pad = max(p.nt, 32);                          // accumulator columns
-  const uint32_t need = (uint32_t)nt_pad + 4 * kXAtoms * (1 + 2);
+  // Tiles of up to 128 tokens alternate between two accumulators, so that the
+  // next tile's MMAs run while one is drained; 256 columns leave room for one.
+  const int nt_pad = max(p.nt, 32);                          // columns of an accumulator
+  const int n_acc = p.nt <= 128 ? 2 : 1;
+  const uint32_t need = (uint32_t)(n_acc * nt_pad) + 4 * kXAtoms * (1 + 2);
   const uint32_t tcols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
   const int stage_bytes = mx_stage_bytes(p.nt);
   const int x_bytes = (p.nt * kXRowBytes + 1023) / 1024 * 1024;
@@ -196,8 +265,10 @@ __global__ void __launch_bounds__(kXThreads, 2)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    mbar_init(&acc_full_bar, 1);
-    mbar_init(&acc_empty_bar, kXEpiWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full_bar[i], 1);
+      mbar_init(&acc_empty_bar[i], kXEpiWarps);
+    }
     mbar_init(&drain_bar, 1);
     abort_s = 0;
     fence_barrier_init();
@@ -242,13 +313,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
   // of this call can give up
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
 
-  int num_tiles;
-  if (p.E == 0) {
-    num_tiles = p.n_wt * p.n_tt;
-  } else {
-    mx_scan_segments(p, seg_start);
-    num_tiles = seg_start[p.E] * p.n_wt;
-  }
+  const MxSegments segs = mx_scan_segments(p, smem + p.stages * stage_bytes);
+  const int num_tiles = mx_num_tiles(p, segs);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -257,7 +323,7 @@ __global__ void __launch_bounds__(kXThreads, 2)
     uint32_t phase = 0, filled = 0, fill_parity = 0;
     bool ok = true;
     for (int t = t_first; ok && t < num_tiles; t += t_step) {
-      const MxTile c = mx_tile(p, seg_start, t);
+      const MxTile c = mx_tile(p, segs, t);
       // token rows in 32-row boxes where a tile is not full (dense tiles:
       // rows past M read as zeros and move no bytes)
       const bool whole = p.E == 0 || c.tokens > p.nt - 32;
@@ -317,16 +383,16 @@ __global__ void __launch_bounds__(kXThreads, 2)
     const uint64_t sfx0 = sdesc_scale_atom(s0 + kXWBytes + x_bytes + kXSfBytes);
     const uint64_t stage_step = (uint64_t)stage_bytes >> 4;
     constexpr uint64_t kAtomStep = kAtomBytes >> 4, kSfStep = kXSfBytes >> 4;
-    const uint32_t sfw_t = tmem + (uint32_t)nt_pad, sfx_t = sfw_t + 4 * kXAtoms;
-    int stage = 0;
+    const uint32_t sfw_t = tmem + (uint32_t)(n_acc * nt_pad), sfx_t = sfw_t + 4 * kXAtoms;
+    int stage = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = t_first; ok && t < num_tiles; t += t_step) {
-      const MxTile c = mx_tile(p, seg_start, t);
+      const MxTile c = mx_tile(p, segs, t);
       const int n_mma = (c.tokens + 15) & ~15;
       const bool two = c.tokens > kRowTile;
       const uint32_t id0 = idesc_mxf4(kXBM, n_mma, 0), id2 = idesc_mxf4(kXBM, n_mma, 2);
-      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty_bar, acc_phase ^ 1u, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty_bar[buf], acc_phase ^ 1u, abort_flag));
       if (!ok) {
         if (elected) {
           *abort_flag = 1;
@@ -335,6 +401,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
         break;
       }
       tc_fence_after();
+      const uint32_t acc_t = tmem + (uint32_t)(buf * nt_pad);
+      uint32_t accumulate = 0;
       for (int i = 0; i < nkt; ++i) {
         ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
         if (!ok) {
@@ -344,34 +412,45 @@ __global__ void __launch_bounds__(kXThreads, 2)
           }
           break;
         }
-        const int atoms = min(kXAtoms, p.groups - (kt0 + i) * kXAtoms);
+        const bool whole = p.groups - (kt0 + i) * kXAtoms >= kXAtoms;     // else K ends with one atom
         if (elected) {
           const uint64_t d = (uint64_t)stage * stage_step;
+          // straight-line code for each of the four shapes of a stage: a
+          // branch per instruction would starve the tensor pipe
+          auto issue = [&](auto n_atoms, auto both) {
+            constexpr int A = decltype(n_atoms)::value;
 #pragma unroll
-          for (int j = 0; j < kXAtoms; ++j) {
-            if (j < atoms) {
+            for (int j = 0; j < A; ++j) {
               tc_cp_scale_atom(sfw_t + 4 * j, sfw0 + d + j * kAtomStep);
               tc_cp_scale_atom(sfx_t + 8 * j, sfx0 + d + j * kAtomStep);
-              if (two) tc_cp_scale_atom(sfx_t + 8 * j + 4, sfx0 + d + kSfStep + j * kAtomStep);
+              if constexpr (decltype(both)::value)
+                tc_cp_scale_atom(sfx_t + 8 * j + 4, sfx0 + d + kSfStep + j * kAtomStep);
             }
-          }
 #pragma unroll
-          for (int j = 0; j < 2 * kXAtoms; ++j)      // 64 elements = 32 bytes of K per MMA, two per atom
-            if (j < 2 * atoms)
-              mma_mxf4(tmem, w0 + d + 2 * j, x0 + d + 2 * j, (j & 1) ? id2 : id0, sfw_t + 4 * (j >> 1),
-                       sfx_t + 8 * (j >> 1), (i | j) != 0);
+            for (int j = 0; j < 2 * A; ++j)          // 64 elements = 32 bytes of K per MMA, two per atom
+              mma_mxf4(acc_t, w0 + d + 2 * j, x0 + d + 2 * j, (j & 1) ? id2 : id0, sfw_t + 4 * (j >> 1),
+                       sfx_t + 8 * (j >> 1), accumulate | j);
+          };
+          if (whole && two) issue(std::integral_constant<int, kXAtoms>{}, std::true_type{});
+          else if (whole) issue(std::integral_constant<int, kXAtoms>{}, std::false_type{});
+          else if (two) issue(std::integral_constant<int, 1>{}, std::true_type{});
+          else issue(std::integral_constant<int, 1>{}, std::false_type{});
           tc_commit(&empty_bar[stage]);
         }
         __syncwarp();
+        accumulate = 1;
         if (++stage == p.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      if (elected) tc_commit(&acc_full_bar);
+      if (elected) tc_commit(&acc_full_bar[buf]);
       __syncwarp();
-      acc_phase ^= 1u;
+      if (++buf == n_acc) {
+        buf = 0;
+        acc_phase ^= 1u;
+      }
     }
     // every MMA completes before tensor memory is freed
     if (elected) {
@@ -386,42 +465,46 @@ __global__ void __launch_bounds__(kXThreads, 2)
     const int n_in = quad * 32 + lane;
     const uint32_t tacc = tmem + ((uint32_t)(quad * 32) << 16);
     float* red = reinterpret_cast<float*>(smem);             // split K: [token][128], the idle stages
+    int buf = 0;
     uint32_t acc_phase = 0;
     for (int t = t_first; t < num_tiles; t += t_step) {
-      const MxTile c = mx_tile(p, seg_start, t);
+      const MxTile c = mx_tile(p, segs, t);
       const int n = c.wt * kXBM + n_in;
-      const bool n_ok = n < p.N;
-      const float bias = p.bias && n_ok && p.splits == 1 ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
-      if (!mbar_wait(&acc_full_bar, acc_phase, abort_flag)) {
+      const float bias = p.bias && n < p.N && p.splits == 1 ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
+      if (!mbar_wait(&acc_full_bar[buf], acc_phase, abort_flag)) {
         *abort_flag = 1;
         atomicExch(p.status, kDevTimeout);
         break;
       }
       tc_fence_after();
+      // handed back as soon as the warp has read its last columns
+      bool held = true;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty_bar[buf]);
+        held = false;
+      };
+#pragma unroll 1
       for (int col = half * 32; col < c.tokens; col += 64) {
         uint32_t r[32];
-        tmem_ld32(tacc + col, r);
+        tmem_ld32(tacc + buf * nt_pad + col, r);
         tmem_ld_wait();
+        if (col + 64 >= c.tokens) release();
         const int cnt = min(32, c.tokens - col);
         if (p.splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (i < cnt) red[(col + i) * kXBM + n_in] = __uint_as_float(r[i]);
-        } else if (n_ok) {
-          const size_t base = (size_t)(c.row0 + col) * (size_t)p.y_stride + n;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < cnt) {
-              float v = __fadd_rn(__uint_as_float(r[i]), bias);
-              if (p.row_weight) v = __fmul_rn(v, p.row_weight[c.row0 + col + i]);
-              mx_store<T>(p.y, base + (size_t)i * (size_t)p.y_stride, v);
-            }
+        } else {
+          mx_store32<T, PLAIN>(p, r, c.row0 + col, cnt, n, bias);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty_bar);
-      acc_phase ^= 1u;
+      if (held) release();
+      if (++buf == n_acc) {
+        buf = 0;
+        acc_phase ^= 1u;
+      }
     }
     __syncwarp();
   }
@@ -429,19 +512,44 @@ __global__ void __launch_bounds__(kXThreads, 2)
     // one tile per cluster (the grid has splits CTAs per tile)
     cluster_sync_all();                                      // every rank's partial sums are in place
     if (warp >= 2 && t_first < num_tiles) {
-      const MxTile c = mx_tile(p, seg_start, t_first);
-      const int tid = threadIdx.x - 64, n_in = tid & (kXBM - 1);
-      const int n = c.wt * kXBM + n_in;
-      if (n < p.N) {
-        const float bias = p.bias ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
-        const uint32_t red = smem_u32(smem);
-        for (int m = rank + p.splits * (tid >> 7); m < c.tokens; m += p.splits * 2) {
-          const uint32_t at = red + (uint32_t)(m * kXBM + n_in) * 4u;
-          float v = ld_shared_cluster_f32(mapa_shared(at, 0));
-          for (int q = 1; q < p.splits; ++q) v = __fadd_rn(v, ld_shared_cluster_f32(mapa_shared(at, (uint32_t)q)));
-          v = __fadd_rn(v, bias);
-          if (p.row_weight) v = __fmul_rn(v, p.row_weight[c.row0 + m]);
-          mx_store<T>(p.y, (size_t)(c.row0 + m) * (size_t)p.y_stride + n, v);
+      // A warp adds one token's 128 sums, four neighbouring outputs a lane;
+      // tokens rank, rank + S, ... are this CTA's.  All ranks' loads are
+      // issued before the first is added: one trip to the neighbours a token.
+      const MxTile c = mx_tile(p, segs, t_first);
+      const int n = c.wt * kXBM + lane * 4;
+      const uint32_t red = smem_u32(smem) + lane * 16;
+      float bias[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        bias[j] = !PLAIN && p.bias && n + j < p.N ? p.bias[(size_t)c.e * p.N + n + j] : 0.0f;
+      for (int m = rank + p.splits * (warp - 2); m < c.tokens; m += p.splits * kXEpiWarps) {
+        float4 v[kXMaxSplits];
+#pragma unroll
+        for (int q = 0; q < kXMaxSplits; ++q)
+          if (q < p.splits) v[q] = ld_shared_cluster_f32x4(mapa_shared(red + (uint32_t)m * (kXBM * 4), (uint32_t)q));
+        float4 z = v[0];
+#pragma unroll
+        for (int q = 1; q < kXMaxSplits; ++q)
+          if (q < p.splits) {
+            z.x = __fadd_rn(z.x, v[q].x);
+            z.y = __fadd_rn(z.y, v[q].y);
+            z.z = __fadd_rn(z.z, v[q].z);
+            z.w = __fadd_rn(z.w, v[q].w);
+          }
+        const float o[4] = {mx_value<PLAIN>(p, __float_as_uint(z.x), c.row0 + m, true, bias[0]),
+                            mx_value<PLAIN>(p, __float_as_uint(z.y), c.row0 + m, true, bias[1]),
+                            mx_value<PLAIN>(p, __float_as_uint(z.z), c.row0 + m, true, bias[2]),
+                            mx_value<PLAIN>(p, __float_as_uint(z.w), c.row0 + m, true, bias[3])};
+        const size_t at = (size_t)(c.row0 + m) * (size_t)p.y_stride + n;
+        if (p.quads && n + 3 < p.N) {
+          if constexpr (T::size == 2)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) = make_uint2(T::pack(o[0], o[1]), T::pack(o[2], o[3]));
+          else
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) mx_store<T>(p.y, at + j, o[j]);
         }
       }
     }
@@ -453,6 +561,312 @@ __global__ void __launch_bounds__(kXThreads, 2)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, tcols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs, for products with many tiles: clusters of two CTAs share one
+// .cta_group::2 MMA of 256 b rows x kPNT tokens (each CTA 128 of the b rows
+// and half of the tokens).  Per 256-element K stage a CTA then loads 16 KiB of
+// b, 24 KiB of tokens and 4 KiB of scales for 768 MMA cycles, 58 bytes a cycle
+// where a CTA by itself needs 102: L2 feeds an SM at 60-odd.  384 tokens (an
+// MMA of 256 and one of 128 columns) instead of 256 is what tensor memory
+// holds beside the scales, and takes 1.5 times fewer accumulator hand-overs.
+// No load is multicast: each CTA reads its own share.
+// ---------------------------------------------------------------------------
+constexpr int kPNT = 384;
+constexpr int kPQ = kPNT / 128;                   // 128-token scale tiles
+constexpr int kPXBytes = kPNT / 2 * kXRowBytes;   // 24 KiB of tokens per CTA
+constexpr int kPSfBytes = kXSfBytes * (1 + kPQ);  // 4 KiB
+constexpr int kPStageBytes = kXWBytes + kPXBytes + kPSfBytes;
+constexpr int kPStages = 5;
+constexpr int kPEpiWarps = 4 * kPQ;               // 128 accumulator columns a thread
+constexpr int kPThreads = 64 + 32 * kPEpiWarps;
+constexpr int kPMaxE = 480;                       // experts whose segment table fits behind the stages
+static_assert(kPStages * kPStageBytes + mx_segment_bytes(kPMaxE) + 1024 <= kXMaxSmem, "pair kernel shared memory");
+constexpr uint32_t kPSfCol = kPNT;                // scales behind the accumulator
+static_assert(kPNT + 4 * kXAtoms * (1 + kPQ) <= 512, "tensor memory");
+
+NVDEV void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa_tmem,
+                         uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem));
+}
+// A CTA that gives up also ends the other CTA's waits.
+NVDEV void mx_give_up_pair(uint32_t* status, volatile int* abort_flag, uint32_t peer_abort) {
+  *abort_flag = 1;
+  atomicExch(status, kDevTimeout);
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(peer_abort) : "memory");
+}
+
+struct MxPairMaps {
+  CUtensorMap w, x, x64;      // codes: boxes of 128, 128 and 64 rows
+  CUtensorMap sfw, sfx;       // scale atoms as rows of 128 words, two per stage
+};
+
+template <typename T, bool PLAIN>
+__global__ void __launch_bounds__(kPThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ MxPairMaps tm, const MxGemmParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full_bar[kPStages];
+  __shared__ __align__(8) uint64_t empty_bar[kPStages];
+  __shared__ __align__(8) uint64_t acc_full_bar;
+  __shared__ __align__(8) uint64_t acc_empty_bar;
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ int abort_s;
+  volatile int* abort_flag = &abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPStages; ++s) {
+      // only the leader's producer arrives on the leader's stage barrier,
+      // expecting the bytes of both CTAs
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(&acc_full_bar, 1);
+    mbar_init(&acc_empty_bar, 2 * kPEpiWarps);               // drained by both CTAs
+    mbar_init(&drain_bar, 1);
+    abort_s = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm.w);
+    prefetch_tmap(&tm.x);
+    prefetch_tmap(&tm.x64);
+    prefetch_tmap(&tm.sfw);
+    prefetch_tmap(&tm.sfx);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_base_s, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();            // both CTAs' barriers exist before either touches the other's
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  const uint32_t peer_abort = mapa_shared(smem_u32(&abort_s), rank ^ 1u);
+  griddep_wait();
+  griddep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
+
+  const MxSegments segs = mx_scan_segments(p, smem + kPStages * kPStageBytes);
+  const int num_tiles = mx_num_tiles(p, segs);
+  const int t_first = (int)(blockIdx.x >> 1), t_step = (int)(gridDim.x >> 1);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t elected = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = t_first; ok && t < num_tiles; t += t_step) {
+      const MxTile c = mx_tile(p, segs, t);
+      const int brow = c.e * p.N + (c.wt * 2 + (int)rank) * kXBM;
+      const int sfw_row = brow / kRowTile * p.groups, sfx_row = c.row0 / kRowTile * p.groups;
+      for (int kt = 0; kt < p.kt_total; ++kt) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
+        if (!ok) {
+          if (elected) mx_give_up_pair(p.status, abort_flag, peer_abort);
+          break;
+        }
+        if (elected) {
+          uint8_t* sW = smem + stage * kPStageBytes;
+          uint8_t* sX = sW + kXWBytes;
+          uint8_t* sSF = sX + kPXBytes;
+          // every load of both CTAs counts on the leader's stage barrier; the
+          // other CTA's bytes may land first (the phase cannot complete
+          // before the leader's arrival)
+          const uint32_t fb = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2u * (uint32_t)kPStageBytes);
+          const int x = kt * kXRowBytes, ka = kt * kXAtoms;
+          tma_load_2d_pair(sSF, &tm.sfw, 0, sfw_row + ka, fb);
+#pragma unroll
+          for (int h = 0; h < kPQ; ++h)
+            tma_load_2d_pair(sSF + kXSfBytes * (1 + h), &tm.sfx, 0, sfx_row + h * p.groups + ka, fb);
+          tma_load_2d_pair(sW, &tm.w, x, brow, fb);
+          // the CTA's half of each MMA's tokens
+          tma_load_2d_pair(sX, &tm.x, x, c.row0 + (int)rank * 128, fb);
+          tma_load_2d_pair(sX + 128 * kXRowBytes, &tm.x64, x, c.row0 + 256 + (int)rank * 64, fb);
+        }
+        __syncwarp();
+        if (++stage == kPStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && leader) {
+    // ------------------------------------------------------------ MMA issuer (the leader's, for both)
+    const uint32_t elected = elect_one();
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t w0 = sdesc_sw128(s0), x0 = sdesc_sw128(s0 + kXWBytes);
+    const uint64_t sf0 = sdesc_scale_atom(s0 + kXWBytes + kPXBytes);
+    constexpr uint64_t kStageStep = kPStageBytes >> 4, kAtomStep = kAtomBytes >> 4, kSfStep = kXSfBytes >> 4;
+    constexpr uint64_t kXHalf = (128 * kXRowBytes) >> 4;
+    const uint32_t sfw_t = tmem + kPSfCol, sfx_t = sfw_t + 4 * kXAtoms;
+    const uint32_t empty_own = mapa_shared(smem_u32(&empty_bar[0]), 0);
+    const uint32_t empty_peer = mapa_shared(smem_u32(&empty_bar[0]), 1);
+    const uint32_t accf_own = mapa_shared(smem_u32(&acc_full_bar), 0);
+    const uint32_t accf_peer = mapa_shared(smem_u32(&acc_full_bar), 1);
+    const uint32_t a0 = idesc_mxf4(256, 256, 0), a2 = idesc_mxf4(256, 256, 2);
+    const uint32_t b0 = idesc_mxf4(256, 128, 0), b2 = idesc_mxf4(256, 128, 2);
+    int stage = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = t_first; ok && t < num_tiles; t += t_step) {
+      const bool third = mx_tile(p, segs, t).tokens > 256;   // the 128-column MMA has real tokens
+      ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty_bar, acc_phase ^ 1u, abort_flag));
+      if (!ok) {
+        if (elected) mx_give_up_pair(p.status, abort_flag, peer_abort);
+        break;
+      }
+      tc_fence_after();
+      uint32_t accumulate = 0;
+      for (int kt = 0; kt < p.kt_total; ++kt) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+        if (!ok) {
+          if (elected) mx_give_up_pair(p.status, abort_flag, peer_abort);
+          break;
+        }
+        const bool whole = p.groups - kt * kXAtoms >= kXAtoms;     // else K ends with one atom
+        if (elected) {
+          const uint64_t d = (uint64_t)stage * kStageStep;
+          // straight-line code for each of the four shapes of a stage: a
+          // branch per instruction would starve the tensor pipe
+          auto issue = [&](auto n_atoms, auto with_third) {
+            constexpr int A = decltype(n_atoms)::value;
+            constexpr bool Third = decltype(with_third)::value;
+#pragma unroll
+            for (int j = 0; j < A; ++j) {
+              tc_cp_scale_atom_pair(sfw_t + 4 * j, sf0 + d + j * kAtomStep);
+#pragma unroll
+              for (int h = 0; h < (Third ? kPQ : 2); ++h)
+                tc_cp_scale_atom_pair(sfx_t + 4 * kPQ * j + 4 * h, sf0 + d + (1 + h) * kSfStep + j * kAtomStep);
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * A; ++j) {
+              const uint32_t sw = sfw_t + 4 * (j >> 1), sx = sfx_t + 4 * kPQ * (j >> 1);
+              mma_mxf4_pair(tmem, w0 + d + 2 * j, x0 + d + 2 * j, (j & 1) ? a2 : a0, sw, sx, accumulate | j);
+              if constexpr (Third)
+                mma_mxf4_pair(tmem + 256, w0 + d + 2 * j, x0 + d + kXHalf + 2 * j, (j & 1) ? b2 : b0, sw, sx + 8,
+                              accumulate | j);
+            }
+          };
+          if (whole && third) issue(std::integral_constant<int, kXAtoms>{}, std::true_type{});
+          else if (whole) issue(std::integral_constant<int, kXAtoms>{}, std::false_type{});
+          else if (third) issue(std::integral_constant<int, 1>{}, std::true_type{});
+          else issue(std::integral_constant<int, 1>{}, std::false_type{});
+          tc_commit_pair(empty_own + 8u * stage);
+          tc_commit_pair(empty_peer + 8u * stage);
+        }
+        __syncwarp();
+        accumulate = 1;
+        if (++stage == kPStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elected) {
+        tc_commit_pair(accf_own);
+        tc_commit_pair(accf_peer);
+      }
+      __syncwarp();
+      acc_phase ^= 1u;
+    }
+    if (elected) {
+      tc_commit_pair(mapa_shared(smem_u32(&drain_bar), 0));
+      volatile int never = 0;
+      mbar_wait(&drain_bar, 0, &never);
+    }
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, part = (warp - 2) >> 2;
+    const int n_in = quad * 32 + lane;
+    const uint32_t tacc = tmem + ((uint32_t)(quad * 32) << 16) + part * 128;
+    const uint32_t acce_leader = mapa_shared(smem_u32(&acc_empty_bar), 0);
+    uint32_t acc_phase = 0;
+    for (int t = t_first; t < num_tiles; t += t_step) {
+      const MxTile c = mx_tile(p, segs, t);
+      const int n = (c.wt * 2 + (int)rank) * kXBM + n_in;
+      const float bias = p.bias && n < p.N ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
+      if (!mbar_wait(&acc_full_bar, acc_phase, abort_flag)) {
+        mx_give_up_pair(p.status, abort_flag, peer_abort);
+        break;
+      }
+      tc_fence_after();
+      const int cnt = c.tokens - part * 128, m0 = c.row0 + part * 128;
+      bool held = true;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(acce_leader);
+        held = false;
+      };
+      if (T::size == 2 && p.pairs && cnt > 0) {
+        // drain the thread's 128 columns into 64 packed words and hand the
+        // accumulator back before any store
+        uint32_t w[64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t r[32];
+          tmem_ld32(tacc + 32 * i, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const int k = 32 * i + j;
+            if constexpr (T::size == 2)
+              w[k / 2] = T::pack(mx_value<PLAIN>(p, r[j], m0 + k, k < cnt, bias),
+                                 mx_value<PLAIN>(p, r[j + 1], m0 + k + 1, k + 1 < cnt, bias));
+          }
+        }
+        release();
+        uint16_t* at = static_cast<uint16_t*>(p.y) + (size_t)(m0 + (n & 1)) * (size_t)p.y_stride + (n & ~1);
+        const size_t step = 2 * (size_t)p.y_stride;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          mx_store_pair(p, w[i], at, cnt - 2 * i, n);
+          at += step;
+        }
+      } else {
+#pragma unroll 1
+        for (int col = 0; col < 128 && col < cnt; col += 32) {
+          uint32_t r[32];
+          tmem_ld32(tacc + col, r);
+          tmem_ld_wait();
+          if (col + 32 >= 128 || col + 32 >= cnt) release();
+          mx_store32<T, PLAIN>(p, r, m0 + col, min(32, cnt - col), n, bias);
+        }
+      }
+      if (held) release();
+      acc_phase ^= 1u;
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves while the other may still arrive on its barriers or
+  // the leader's MMAs may still read its shared memory
+  cluster_sync_all();
+  if (*abort_flag) {
+    // copies issued before a give-up may still be landing here: they finish within microseconds
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -488,34 +902,74 @@ struct MxGemmArgs {
 // Tile width, pipeline depth and K splits of a product (host arithmetic).
 struct MxPlan {
   int nt, stages, splits, ctas_per_sm;
+  bool pair;
 };
+
+// Tiles of 128 or 256 tokens on one CTA, or of 384 on a pair: the one whose
+// waves are estimated to end first, from measurements at K = 1024 to 6144 of
+// one to four waves (one B200; us for a wave's K stages and hand-over, and
+// once for start and end).  Measured at 6144 (24 stages), waves x time:
+//   128 tokens  1: 16.5  2: 25.0  3: 35.0  4: 44.5
+//   256 tokens  1: 18.5  2: 31.8
+//   pair        1: 22.6  2: 34.6  5: 74.4
+// and at 1024 (4 stages) 1: 8.3, 10.3 and 12.4.
+struct MxWave {
+  int nt;
+  double stage, wave, once;
+};
+constexpr MxWave kMxWaves[3] = {{128, 0.30, 2.3, 6.0}, {256, 0.40, 3.4, 5.5}, {kPNT, 0.36, 3.4, 8.0}};
+
 static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
-  MxPlan pl;
-  const int n_wt = (N + kXBM - 1) / kXBM;
   const int kt = (mx_groups(K) + kXAtoms - 1) / kXAtoms;
-  if (E == 0 && M <= kXMaxNT) {
-    pl.nt = (M + 15) / 16 * 16;
-  } else {
-    const long long wide = (long long)n_wt * std::max(1, E) * ((M / std::max(1, E) + kXMaxNT - 1) / kXMaxNT);
-    pl.nt = wide < sms ? 128 : kXMaxNT;
+  const int n_wt = (N + kXBM - 1) / kXBM;
+  const int experts = std::max(1, E);
+  const long long per = ((long long)M + experts - 1) / experts;      // tokens an expert, taken as even
+  MxPlan pl;
+  pl.splits = pl.ctas_per_sm = 1;
+  int best = 0;
+  double best_us = 0;
+  for (int i = 0; i < (E <= kPMaxE ? 3 : 2); ++i) {
+    const MxWave& w = kMxWaves[i];
+    const bool pair = i == 2;
+    const long long tiles = (long long)(pair ? (n_wt + 1) / 2 : n_wt) * experts * ((per + w.nt - 1) / w.nt);
+    const long long slots = pair ? sms / 2 : sms;
+    const double us = w.once + (double)((tiles + slots - 1) / slots) * (w.stage * kt + w.wave);
+    if (i == 0 || us < best_us) {
+      best = i;
+      best_us = us;
+    }
   }
+  pl.pair = best == 2;
+  pl.nt = kMxWaves[best].nt;
+  if (pl.pair) {
+    pl.stages = kPStages;
+    return pl;
+  }
+  // a single token tile is no wider than its tokens
+  if (E == 0 && M <= pl.nt) pl.nt = (M + 15) / 16 * 16;
+  // Few tokens: two CTAs on an SM, and K split over a cluster while there are
+  // SMs for it.  Measured at N = K = 6144 (48 tiles) and one token, splits of
+  // 1, 2, 3, 4, 6, 8: 14.4, 10.8, 10.3, 10.3, 14.5, 14.5 us; at N = 1024 (8
+  // tiles) 12.7, 10.3, 8.9, 8.3, 8.3, 8.3; wider tiles, at one CTA an SM (128
+  // tokens, 48 tiles): 15.6, 14.4, then 22 and more, as clusters of three and
+  // more no longer fit at once.
   pl.ctas_per_sm = pl.nt <= 64 ? 2 : 1;
-  const int room = (pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024;
+  const int room = (pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - mx_segment_bytes(E);
   pl.stages = std::min(kXMaxStages, room / mx_stage_bytes(pl.nt));
-  pl.splits = 1;
   if (E == 0) {
     const long long tiles = (long long)n_wt * ((M + pl.nt - 1) / pl.nt);
-    if (tiles < sms) pl.splits = (int)std::min<long long>({8, (long long)sms * pl.ctas_per_sm / tiles, (kt + 1) / 2});
-    pl.splits = std::max(1, pl.splits);
+    const long long most = pl.ctas_per_sm == 2 || tiles * 4 <= sms / 2 ? 4 : 2;
+    pl.splits = (int)std::max(1ll, std::min({most, sms / tiles, (long long)(kt + 1) / 2}));
   }
   return pl;
 }
 
-template <typename T>
-static nvfp4_status run_mx_gemm(const MxGemmArgs& a, const MxPlan& pl, int sms, const CUtensorMap& tmW,
+template <typename T, bool PLAIN>
+static nvfp4_status run_mx_gemm(const MxPlan& pl, int sms, const CUtensorMap& tmW,
                                 const CUtensorMap& tmX, const CUtensorMap& tmX32, const MxGemmParams& p,
                                 long long tiles, cudaStream_t s) {
-  NV_CHECK(opt_in_smem<mx_gemm_kernel<T>>());
+  constexpr auto kernel = mx_gemm_kernel<T, PLAIN>;
+  NV_CHECK(opt_in_smem<kernel>());
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -532,10 +986,61 @@ static nvfp4_status run_mx_gemm(const MxGemmArgs& a, const MxPlan& pl, int sms, 
   cfg.blockDim = dim3(kXThreads);
   cfg.gridDim = dim3((unsigned)(pl.splits > 1 ? tiles * pl.splits
                                               : std::max(1ll, std::min<long long>(tiles, (long long)sms * pl.ctas_per_sm))));
-  cfg.dynamicSmemBytes = (size_t)pl.stages * mx_stage_bytes(pl.nt) + 1024;
+  cfg.dynamicSmemBytes = (size_t)pl.stages * mx_stage_bytes(pl.nt) + mx_segment_bytes(p.E) + 1024;
   cfg.stream = s;
-  (void)a;
-  return check_cuda(cudaLaunchKernelEx(&cfg, mx_gemm_kernel<T>, tmW, tmX, tmX32, p), "mx_gemm_kernel");
+  return check_cuda(cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, tmX32, p), "mx_gemm_kernel");
+}
+
+template <typename T, bool PLAIN>
+static nvfp4_status run_mx_gemm_pair(const MxPairMaps& tm, const MxGemmParams& p, long long tiles, cudaStream_t s) {
+  constexpr auto kernel = mx_gemm_pair_kernel<T, PLAIN>;
+  NV_CHECK(opt_in_smem<kernel>());
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = kPStages * kPStageBytes + mx_segment_bytes(p.E) + 1024;
+  cfg.stream = s;
+  // the grid is persistent: as many pairs as can be resident at once
+  static std::mutex mu;
+  static int resident[64] = {};
+  int dev = 0, n = 0;
+  NV_CHECK(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const bool kept = dev >= 0 && dev < 64;
+    n = kept ? resident[dev] : 0;
+    if (n == 0) {
+      int sms = 0;
+      NV_CHECK(device_sm_count(&sms));
+      cfg.gridDim = dim3(2 * (sms / 2));
+      NV_CHECK(check_cuda(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg),
+                          "cudaOccupancyMaxActiveClusters"));
+      NV_REQUIRE(n >= 1, NVFP4_ERR_CUDA, "mx_gemm_pair_kernel: no cluster of two CTAs can be resident");
+      if (kept) resident[dev] = n;
+    }
+  }
+  cfg.gridDim = dim3((unsigned)(2 * std::max(1ll, std::min<long long>(n, tiles))));
+  cfg.numAttrs = 2;
+  return check_cuda(cudaLaunchKernelEx(&cfg, kernel, tm, p), "mx_gemm_pair_kernel");
+}
+
+// Calls f(output type tag, whether there is neither bias nor row weight).
+template <typename F>
+static nvfp4_status with_output(const MxGemmArgs& a, F&& f) {
+  auto by_plain = [&](auto tag) -> nvfp4_status {
+    return a.bias || a.row_weight ? f(tag, std::false_type{}) : f(tag, std::true_type{});
+  };
+  if (a.out_dtype == MXFP4_DTYPE_BF16) return by_plain(Bf16{});
+  if (a.out_dtype == MXFP4_DTYPE_F16) return by_plain(F16{});
+  return by_plain(F32{});
 }
 
 static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
@@ -548,12 +1053,15 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   p.E = a.E;
   p.groups = mx_groups(a.K);
   p.kt_total = (p.groups + kXAtoms - 1) / kXAtoms;
-  p.n_wt = (a.N + kXBM - 1) / kXBM;
+  p.n_wt = pl.pair ? (a.N + 2 * kXBM - 1) / (2 * kXBM) : (a.N + kXBM - 1) / kXBM;
   p.nt = pl.nt;
   p.n_tt = a.E ? 0 : (a.M + pl.nt - 1) / pl.nt;
   p.stages = pl.stages;
   p.splits = pl.splits;
   p.early_b = a.early_b && a.E == 0;
+  const int elem = mx_elem_size(a.out_dtype), access = row_access_bytes(a.y, a.M > 1 ? a.y_stride * elem : 0, elem);
+  p.pairs = elem == 2 && access >= 4;
+  p.quads = access >= 4 * elem;
   p.expert_offsets = a.expert_offsets;
   p.expert_counts = a.expert_counts;
   p.a_sf = a.a_scales;
@@ -566,6 +1074,22 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   // tiles at most: each expert may end in a partly filled token tile
   const long long tiles = (long long)p.n_wt * (a.E ? (a.M + pl.nt - 1) / pl.nt + a.E : p.n_tt);
   const uint64_t inner = (uint64_t)mx_row_bytes(a.K);
+  if (pl.pair) {
+    MxPairMaps tm;
+    const uint64_t brows = (uint64_t)std::max(1, a.E) * (uint64_t)a.N;
+    NV_CHECK(make_tmap_2d(&tm.w, a.b_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner, brows, inner, kXRowBytes, kXBM));
+    NV_CHECK(make_tmap_2d(&tm.x, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner, (uint64_t)a.M, inner, kXRowBytes, 128));
+    NV_CHECK(make_tmap_2d(&tm.x64, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner, (uint64_t)a.M, inner, kXRowBytes, 64));
+    // scale atoms as rows of 128 words; a box that reaches past the last atom
+    // of a row tile reads the next tile's (or zeros), which no MMA uses
+    NV_CHECK(make_tmap_2d(&tm.sfw, a.b_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128,
+                          (brows + 127) / 128 * (uint64_t)p.groups, kAtomBytes, 128, kXAtoms, false));
+    NV_CHECK(make_tmap_2d(&tm.sfx, a.a_scales, CU_TENSOR_MAP_DATA_TYPE_UINT32, 128,
+                          ((uint64_t)a.M + 127) / 128 * (uint64_t)p.groups, kAtomBytes, 128, kXAtoms, false));
+    return with_output(a, [&](auto tag, auto plain) -> nvfp4_status {
+      return run_mx_gemm_pair<decltype(tag), decltype(plain)::value>(tm, p, tiles, s);
+    });
+  }
   CUtensorMap tmW, tmX, tmX32;
   NV_CHECK(make_tmap_2d(&tmW, a.b_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner,
                         (uint64_t)std::max(1, a.E) * (uint64_t)a.N, inner, kXRowBytes, kXBM));
@@ -577,11 +1101,9 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   } else {
     tmX32 = tmX;
   }
-  switch (a.out_dtype) {
-    case MXFP4_DTYPE_BF16: return run_mx_gemm<Bf16>(a, pl, sms, tmW, tmX, tmX32, p, tiles, s);
-    case MXFP4_DTYPE_F16: return run_mx_gemm<F16>(a, pl, sms, tmW, tmX, tmX32, p, tiles, s);
-    default: return run_mx_gemm<F32>(a, pl, sms, tmW, tmX, tmX32, p, tiles, s);
-  }
+  return with_output(a, [&](auto tag, auto plain) -> nvfp4_status {
+    return run_mx_gemm<decltype(tag), decltype(plain)::value>(pl, sms, tmW, tmX, tmX32, p, tiles, s);
+  });
 }
 
 static nvfp4_status check_product(const char* name, int M, const uint8_t* b_codes, const uint8_t* b_scales, int N,
@@ -691,4 +1213,13 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long lo
   cudaStream_t s = as_stream(stream);
   NV_CHECK(launch_mx_quantize(x, dtype, rows, K, row_stride, perm, M, NVFP4_LAYOUT_TILED, l.codes, l.scales, s));
   return launch_mx_gemm(g, s);
+}
+
+extern "C" int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages) {
+  if (M < 1 || N < 1 || K < 1 || E < 0) return -1;
+  const MxPlan pl = plan_mx_gemm(M, N, K, E, 148);
+  if (splits) *splits = pl.splits;
+  if (pair) *pair = pl.pair ? 1 : 0;
+  if (stages) *stages = pl.stages;
+  return pl.nt;
 }

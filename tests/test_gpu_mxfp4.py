@@ -181,7 +181,9 @@ def product_bound(a, b, ref, dtype, row_weight=None, bias=None):
 MNK = [(1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16, 256, 128), (17, 500, 160),
        (31, 64, 256), (32, 129, 288), (33, 1000, 544), (64, 384, 1024), (65, 128, 100), (100, 300, 2048),
        (128, 128, 512), (129, 255, 320), (200, 1024, 640), (256, 256, 256), (257, 130, 224), (300, 700, 384),
-       (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000)]
+       (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000),
+       # on CTA pairs (tests/test_mxfp4.py checks that these sizes reach them), K ending with one atom and two
+       (1536, 4096, 96), (1500, 3999, 300), (3000, 2049, 416)]
 
 
 @pytest.mark.parametrize("M,N,K", MNK)
@@ -219,7 +221,7 @@ def test_matmul_bias_row_weight_and_strided_out():
     require_cuda()
     c = capi()
     rng = np.random.default_rng(5)
-    for M, N, K in [(3, 200, 320), (40, 130, 96), (300, 300, 256)]:
+    for M, N, K in [(3, 200, 320), (3, 200, 2048), (40, 130, 96), (300, 300, 256), (1500, 3999, 300)]:
         a, av = operand(M, K, 1)
         b, bv = operand(N, K, 2)
         bias = rng.standard_normal(N).astype(np.float32)
@@ -233,19 +235,20 @@ def test_matmul_bias_row_weight_and_strided_out():
         assert (big[:, :5] == 7.0).all() and (big[:, 5 + N:] == 7.0).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 1500])
 def test_a_nan_block_reaches_its_row_only(M):
     require_cuda()
     c = capi()
     a, av = operand(M, 300, 3)
-    b, bv = operand(200, 300, 4)
+    N = 200 if M < 1500 else 3999
+    b, bv = operand(N, 300, 4)
     clean = c.mxfp4_matmul(a, b)
     at = int(mxfp4.tiled_index(M, 300)[M - 1, 9])              # the last, partly filled block
     a.scales[at] = 255
     y = c.mxfp4_matmul(a, b)
     assert torch.isnan(y[M - 1]).all() and torch.equal(y[:M - 1], clean[:M - 1])
     a.scales[at] = 127
-    b.scales[int(mxfp4.tiled_index(200, 300)[131, 0])] = 255
+    b.scales[int(mxfp4.tiled_index(N, 300)[131, 0])] = 255
     y = c.mxfp4_matmul(a, b)
     assert torch.isnan(y[:, 131]).all() and not torch.isnan(y[:, :131]).any() and not torch.isnan(y[:, 132:]).any()
 
@@ -254,7 +257,7 @@ def test_padding_bytes_do_not_matter():
     """Scale bytes of padding rows may hold anything, NaN included."""
     require_cuda()
     c = capi()
-    for M, N, K in [(3, 70, 100), (150, 260, 300)]:
+    for M, N, K in [(3, 70, 100), (150, 260, 300), (1500, 3999, 300)]:
         a, av = operand(M, K, 8)
         b, bv = operand(N, K, 9)
         want = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
@@ -281,6 +284,8 @@ def grouped_case(counts, gaps, N, K, seed):
     ([3] * 40, [0] * 40, 128, 512),
     ([1000, 0, 257], [0, 0, 0], 384, 160),
     ([0, 0, 0], [0, 1, 0], 128, 96),
+    ([1000, 0, 385, 2900], [0, 0, 0, 0], 2048, 288),        # on CTA pairs
+    ([1500, 1024, 1, 2000], [0, 0, 1, 0], 1920, 160),        # pairs, an odd number of 128-row b tiles per expert
 ])
 def test_grouped_matmul(counts, gaps, N, K):
     require_cuda()
@@ -336,7 +341,7 @@ def test_linear_is_quantize_then_matmul():
 def test_results_do_not_change_from_run_to_run():
     require_cuda()
     c = capi()
-    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024)]:
+    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024), (1536, 4096, 96)]:
         a, _ = operand(M, K, 1)
         b, _ = operand(N, K, 2)
         first = c.mxfp4_matmul(a, b, out_dtype=torch.float32)

@@ -144,6 +144,45 @@ def test_product_refusals():
     assert c.mxfp4_linear_workspace_size(-1, 64) == 0
 
 
+def test_product_plans():
+    """Host arithmetic: every plan fits the kernels' limits, and the sizes
+    that the GPU tests use reach each of their variants."""
+    c = capi()
+    plan = c.nvfp4_test_mxfp4_plan
+    sizes = (1, 2, 15, 16, 17, 64, 65, 128, 129, 255, 256, 257, 384, 385, 1000, 4096, 8192, 100000)
+    for M in sizes:
+        for N in sizes:
+            for K in (1, 32, 256, 257, 2048, 6144, 16384):
+                nt, splits, pair, stages = plan(M, N, K)
+                kt = -(-K // 256)
+                assert 1 <= splits <= 8 and splits <= kt
+                assert nt % 16 == 0 and (nt == 384) == pair
+                assert nt >= min(M, 128) and (nt % 128 == 0 or nt >= M)    # a narrow tile is the only one
+                assert stages >= 3
+                if not pair:
+                    # two accumulators up to 128 columns, then the scales: within tensor memory
+                    acc = max(nt, 32) * (2 if nt <= 128 else 1)
+                    assert acc + 24 <= 512 and nt <= 256
+                    # the split's partial sums fit the stages they overlay
+                    stage = 16384 + nt * 128 + 1024 * (1 + -(-nt // 128))
+                    assert splits == 1 or nt * 512 <= stages * stage
+                    assert stages * stage + 1024 <= (227 * 1024 - 256 if nt > 64 else 114 * 1024 - 1024 - 256)
+            for E in (1, 8, 80, 481, 1024):
+                if N % 128 == 0 and M % 128 == 0:
+                    nt, splits, pair, stages = plan(M, N, 2048, E)
+                    assert nt in (128, 256, 384) and splits == 1 and not (pair and E > 480)
+                    stage = 16384 + nt * 128 + 1024 * (1 + nt // 128)
+                    if not pair:
+                        assert stages * stage + (3 * E + 1) * 4 + 1024 <= 227 * 1024 - 256
+    assert plan(1, 6144, 512)[1] == 1 and plan(16, 128, 6144)[1] == 4 and plan(100, 300, 2048)[1] == 4
+    assert plan(1, 1000, 4096) == (16, 4, False, 5)
+    for M, N, K in ((1536, 4096, 96), (1500, 3999, 300), (3000, 2049, 416)):
+        assert plan(M, N, K)[2]
+    assert plan(4480, 2048, 288, 4)[2] and plan(4864, 1920, 160, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
+    with pytest.raises(ValueError):
+        plan(0, 1, 1)
+
+
 def test_balance_refusals():
     lib = capi().lib
 
