@@ -149,10 +149,13 @@ NVDEV void store_words8(void* p, const uint32_t* w) {
 inline int mx_elem_size(int dtype) { return dtype == MXFP4_DTYPE_F32 ? 4 : 2; }
 inline bool mx_dtype_ok(int dtype) { return dtype >= MXFP4_DTYPE_BF16 && dtype <= MXFP4_DTYPE_F32; }
 
-// Queues mxfp4_quantize on checked arguments (used by the product too).
+// Queues mxfp4_quantize on checked arguments (used by the product too, which
+// with expert_counts needs no codes of rows outside the experts' tokens: those
+// of them that have no source are left unwritten).
 nvfp4_status launch_mx_quantize(const void* x, int dtype, int rows, int cols, long long row_stride,
                                 const int32_t* perm, int out_rows, int layout, uint8_t* codes, uint8_t* scales,
-                                cudaStream_t s);
+                                cudaStream_t s, const int32_t* expert_offsets = nullptr,
+                                const int32_t* expert_counts = nullptr, int E = 0);
 nvfp4_status check_mx_source(const char* name, const void* x, int dtype, int rows, int cols, long long row_stride);
 
 }  // namespace nvfp4moe

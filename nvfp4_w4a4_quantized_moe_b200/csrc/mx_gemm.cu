@@ -181,13 +181,22 @@ NVDEV void mx_store(void* y, size_t i, float v) {
   else static_cast<float*>(y)[i] = v;
 }
 
-// bias and row weight of one accumulator value (token m, the thread's column).
+// Bias and row weight of one accumulator value.  PLAIN: neither.
 template <bool PLAIN>
-NVDEV float mx_value(const MxGemmParams& p, uint32_t acc, int m, bool real, float bias) {
+NVDEV float mx_value(uint32_t acc, float weight, float bias) {
   const float v = __uint_as_float(acc);
-  if constexpr (PLAIN) return v;
-  const float s = __fadd_rn(v, bias);
-  return p.row_weight ? __fmul_rn(s, real ? __ldg(p.row_weight + m) : 0.0f) : s;
+  return PLAIN ? v : __fmul_rn(__fadd_rn(v, bias), weight);
+}
+// The row weights of 32 tokens from m0 on, one a lane (1 where there are
+// none); mx_weight broadcasts token i's.
+template <bool PLAIN>
+NVDEV float mx_load_weight(const MxGemmParams& p, int m0, int cnt) {
+  const int lane = threadIdx.x & 31;
+  return !PLAIN && p.row_weight && lane < cnt ? __ldg(p.row_weight + m0 + lane) : 1.0f;
+}
+template <bool PLAIN>
+NVDEV float mx_weight(float held, int i) {
+  return PLAIN ? 1.0f : __shfl_sync(0xffffffffu, held, i);
 }
 
 // 16-bit outputs of two neighbouring tokens m, m + 1 of the thread's column n,
@@ -206,27 +215,27 @@ NVDEV void mx_store_pair(const MxGemmParams& p, uint32_t word, uint16_t* at, int
 }
 
 // A thread's 32 accumulator columns (tokens m0 ..., the first `cnt` real) of
-// output column n.
+// output column n; `held` from mx_load_weight.
 template <typename T, bool PLAIN>
-NVDEV void mx_store32(const MxGemmParams& p, const uint32_t* r, int m0, int cnt, int n, float bias) {
+NVDEV void mx_store32(const MxGemmParams& p, const uint32_t* r, int m0, int cnt, int n, float bias, float held) {
   if constexpr (T::size == 2) {
     if (p.pairs) {
       uint16_t* at = static_cast<uint16_t*>(p.y) + (size_t)(m0 + (n & 1)) * (size_t)p.y_stride + (n & ~1);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        mx_store_pair(p, T::pack(mx_value<PLAIN>(p, r[i], m0 + i, i < cnt, bias),
-                                 mx_value<PLAIN>(p, r[i + 1], m0 + i + 1, i + 1 < cnt, bias)),
+        mx_store_pair(p, T::pack(mx_value<PLAIN>(r[i], mx_weight<PLAIN>(held, i), bias),
+                                 mx_value<PLAIN>(r[i + 1], mx_weight<PLAIN>(held, i + 1), bias)),
                       at, cnt - i, n);
         at += 2 * (size_t)p.y_stride;
       }
       return;
     }
   }
-  if (n >= p.N) return;
   size_t at = (size_t)m0 * (size_t)p.y_stride + n;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    if (i < cnt) mx_store<T>(p.y, at, mx_value<PLAIN>(p, r[i], m0 + i, true, bias));
+    const float w = mx_weight<PLAIN>(held, i);               // every lane takes part in the shuffle
+    if (i < cnt && n < p.N) mx_store<T>(p.y, at, mx_value<PLAIN>(r[i], w, bias));
     at += (size_t)p.y_stride;
   }
 }
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(kXThreads, 2)
     for (int t = t_first; t < num_tiles; t += t_step) {
       const MxTile c = mx_tile(p, segs, t);
       const int n = c.wt * kXBM + n_in;
-      const float bias = p.bias && n < p.N && p.splits == 1 ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
+      const float bias = !PLAIN && p.bias && n < p.N && p.splits == 1 ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
       if (!mbar_wait(&acc_full_bar[buf], acc_phase, abort_flag)) {
         *abort_flag = 1;
         atomicExch(p.status, kDevTimeout);
@@ -489,15 +498,16 @@ __global__ void __launch_bounds__(kXThreads, 2)
       for (int col = half * 32; col < c.tokens; col += 64) {
         uint32_t r[32];
         tmem_ld32(tacc + buf * nt_pad + col, r);
+        const int cnt = min(32, c.tokens - col);
+        const float weights = mx_load_weight<PLAIN>(p, c.row0 + col, cnt);
         tmem_ld_wait();
         if (col + 64 >= c.tokens) release();
-        const int cnt = min(32, c.tokens - col);
         if (p.splits > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (i < cnt) red[(col + i) * kXBM + n_in] = __uint_as_float(r[i]);
         } else {
-          mx_store32<T, PLAIN>(p, r, c.row0 + col, cnt, n, bias);
+          mx_store32<T, PLAIN>(p, r, c.row0 + col, cnt, n, bias, weights);
         }
       }
       if (held) release();
@@ -536,10 +546,11 @@ __global__ void __launch_bounds__(kXThreads, 2)
             z.z = __fadd_rn(z.z, v[q].z);
             z.w = __fadd_rn(z.w, v[q].w);
           }
-        const float o[4] = {mx_value<PLAIN>(p, __float_as_uint(z.x), c.row0 + m, true, bias[0]),
-                            mx_value<PLAIN>(p, __float_as_uint(z.y), c.row0 + m, true, bias[1]),
-                            mx_value<PLAIN>(p, __float_as_uint(z.z), c.row0 + m, true, bias[2]),
-                            mx_value<PLAIN>(p, __float_as_uint(z.w), c.row0 + m, true, bias[3])};
+        const float w = !PLAIN && p.row_weight ? __ldg(p.row_weight + c.row0 + m) : 1.0f;
+        const float o[4] = {mx_value<PLAIN>(__float_as_uint(z.x), w, bias[0]),
+                            mx_value<PLAIN>(__float_as_uint(z.y), w, bias[1]),
+                            mx_value<PLAIN>(__float_as_uint(z.z), w, bias[2]),
+                            mx_value<PLAIN>(__float_as_uint(z.w), w, bias[3])};
         const size_t at = (size_t)(c.row0 + m) * (size_t)p.y_stride + n;
         if (p.quads && n + 3 < p.N) {
           if constexpr (T::size == 2)
@@ -799,13 +810,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
     for (int t = t_first; t < num_tiles; t += t_step) {
       const MxTile c = mx_tile(p, segs, t);
       const int n = (c.wt * 2 + (int)rank) * kXBM + n_in;
-      const float bias = p.bias && n < p.N ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
+      const float bias = !PLAIN && p.bias && n < p.N ? p.bias[(size_t)c.e * p.N + n] : 0.0f;
+      // loaded before the accumulator is ready
+      const int cnt = c.tokens - part * 128, m0 = c.row0 + part * 128;
+      float weights[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) weights[i] = mx_load_weight<PLAIN>(p, m0 + 32 * i, cnt - 32 * i);
       if (!mbar_wait(&acc_full_bar, acc_phase, abort_flag)) {
         mx_give_up_pair(p.status, abort_flag, peer_abort);
         break;
       }
       tc_fence_after();
-      const int cnt = c.tokens - part * 128, m0 = c.row0 + part * 128;
       bool held = true;
       auto release = [&]() {
         tc_fence_before();
@@ -824,10 +839,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const int k = 32 * i + j;
             if constexpr (T::size == 2)
-              w[k / 2] = T::pack(mx_value<PLAIN>(p, r[j], m0 + k, k < cnt, bias),
-                                 mx_value<PLAIN>(p, r[j + 1], m0 + k + 1, k + 1 < cnt, bias));
+              w[16 * i + j / 2] = T::pack(mx_value<PLAIN>(r[j], mx_weight<PLAIN>(weights[i], j), bias),
+                                          mx_value<PLAIN>(r[j + 1], mx_weight<PLAIN>(weights[i], j + 1), bias));
           }
         }
         release();
@@ -845,7 +859,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tmem_ld32(tacc + col, r);
           tmem_ld_wait();
           if (col + 32 >= 128 || col + 32 >= cnt) release();
-          mx_store32<T, PLAIN>(p, r, m0 + col, min(32, cnt - col), n, bias);
+          const float h = col == 0 ? weights[0] : col == 32 ? weights[1] : col == 64 ? weights[2] : weights[3];
+          mx_store32<T, PLAIN>(p, r, m0 + col, min(32, cnt - col), n, bias, h);
         }
       }
       if (held) release();
@@ -906,24 +921,28 @@ struct MxPlan {
 };
 
 // Tiles of 128 or 256 tokens on one CTA, or of 384 on a pair: the one whose
-// waves are estimated to end first, from measurements at K = 1024 to 6144 of
-// one to four waves (one B200; us for a wave's K stages and hand-over, and
-// once for start and end).  Measured at 6144 (24 stages), waves x time:
-//   128 tokens  1: 16.5  2: 25.0  3: 35.0  4: 44.5
-//   256 tokens  1: 18.5  2: 31.8
-//   pair        1: 22.6  2: 34.6  5: 74.4
-// and at 1024 (4 stages) 1: 8.3, 10.3 and 12.4.
+// waves are estimated to end first, fitted to measurements of one to seven
+// waves (one B200; us for each K stage and hand-over of a wave, and once for
+// start and end).  Measured, waves: us
+//   K = 6144 (24 stages)   128 tokens  1: 12.5  2: 20.7  3: 29.4  4: 37.4  7: 61.8
+//                          256 tokens  1: 15.7  2: 28.4  4: 53.5
+//                          pair        1: 18.7  2: 29.6  3: 41.5
+//   K = 1024 (4 stages)    128 tokens  1: 6.7   2: 8.3   4: 13.0
+//                          256 tokens  1: 8.2   2: 13.0
+//                          pair        1: 9.4   2: 14.0
 struct MxWave {
   int nt;
   double stage, wave, once;
 };
-constexpr MxWave kMxWaves[3] = {{128, 0.30, 2.3, 6.0}, {256, 0.40, 3.4, 5.5}, {kPNT, 0.36, 3.4, 8.0}};
+constexpr MxWave kMxWaves[3] = {{128, 0.30, 0.9, 4.5}, {256, 0.385, 3.2, 3.2}, {kPNT, 0.32, 3.3, 6.5}};
 
 static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   const int kt = (mx_groups(K) + kXAtoms - 1) / kXAtoms;
   const int n_wt = (N + kXBM - 1) / kXBM;
   const int experts = std::max(1, E);
-  const long long per = ((long long)M + experts - 1) / experts;      // tokens an expert, taken as even
+  // tokens an expert, taken as even; grouped rows hold up to 127 of padding an
+  // expert (moe_route's capacity has that many)
+  const long long per = E == 0 ? M : std::max(16ll, (long long)M / E - 127);
   MxPlan pl;
   pl.splits = pl.ctas_per_sm = 1;
   int best = 0;
@@ -949,10 +968,11 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   if (E == 0 && M <= pl.nt) pl.nt = (M + 15) / 16 * 16;
   // Few tokens: two CTAs on an SM, and K split over a cluster while there are
   // SMs for it.  Measured at N = K = 6144 (48 tiles) and one token, splits of
-  // 1, 2, 3, 4, 6, 8: 14.4, 10.8, 10.3, 10.3, 14.5, 14.5 us; at N = 1024 (8
-  // tiles) 12.7, 10.3, 8.9, 8.3, 8.3, 8.3; wider tiles, at one CTA an SM (128
-  // tokens, 48 tiles): 15.6, 14.4, then 22 and more, as clusters of three and
-  // more no longer fit at once.
+  // 1, 2, 3, 4, 6, 8: 10.8, 7.8, 7.6, 7.0, 11.4, 11.2 us; at N = 1024 (8
+  // tiles) 10.2, 6.9, 5.8, 5.1, 4.7, 4.4; at N = 5001, K = 2010 (40 tiles) 6.0,
+  // 5.7, 5.5, 6.6, 6.7, 11.0; wider tiles, at one CTA an SM (128 tokens, 48
+  // tiles): 12.2, 11.2, then 17 and more, as clusters of three and more no
+  // longer fit at once.
   pl.ctas_per_sm = pl.nt <= 64 ? 2 : 1;
   const int room = (pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - mx_segment_bytes(E);
   pl.stages = std::min(kXMaxStages, room / mx_stage_bytes(pl.nt));
@@ -1211,7 +1231,8 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long lo
   // only behind everything queued earlier, which may have written b
   g.early_b = true;
   cudaStream_t s = as_stream(stream);
-  NV_CHECK(launch_mx_quantize(x, dtype, rows, K, row_stride, perm, M, NVFP4_LAYOUT_TILED, l.codes, l.scales, s));
+  NV_CHECK(launch_mx_quantize(x, dtype, rows, K, row_stride, perm, M, NVFP4_LAYOUT_TILED, l.codes, l.scales, s,
+                              expert_offsets, expert_counts, E));
   return launch_mx_gemm(g, s);
 }
 

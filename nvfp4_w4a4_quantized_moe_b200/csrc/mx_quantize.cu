@@ -7,10 +7,10 @@
 // and the one rounding is the hardware's E2M1 conversion.
 //
 // Measured on one B200 as a share of its copy rate (6,449 GB/s):
-//   65536 x 6144 bf16: quantise 158 us (100 %), transposed 193 us (82 %),
-//   read-back 154 us (103 %); 32768 x 6144 fp32: 139 us (102 %), 164 us
-//   (86 %), 139 us (102 %); 8192 x 6144 bf16 (inside L2's reach, a few us of
-//   launch and tail): 24, 31 and 23 us.
+//   65536 x 6144 bf16: quantise 158 us (100 %), transposed 199 us (80 %),
+//   read-back 154 us (103 %); 32768 x 6144 fp32: 139 us (102 %), 149 us
+//   (95 %), 139 us (102 %); 8192 x 6144 bf16: 22 us (91 %), 24 us (81 %),
+//   21 us (95 %).
 // The first form, with 16-byte loads, two packed maxima less and a 32-bit
 // division a unit, took 259 and 202 us at 65536 x 6144.
 #include <type_traits>
@@ -162,8 +162,44 @@ NVDEV float share_value(const uint32_t* w, int i) {
   else return __uint_as_float(w[i]);
 }
 
+// Quantises the unit (row, group) from its lanes' shares; every lane of the
+// warp takes part, `real` units are written.  The unit's four scale bytes
+// leave as one word.
+template <typename T>
+NVDEV void quantize_unit(const uint32_t* w, int row, int grp, bool real, int cols, int groups, int tiled,
+                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>();
+  const int l = threadIdx.x & (LPU - 1), blocks = mx_blocks(cols);
+  const uint32_t s = mx_scale(share_amax<T>(w));
+  const float inv = mx_inv_scale(s);
+  uint32_t q[EPL / 8];
+#pragma unroll
+  for (int h = 0; h < EPL / 8; ++h) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = share_value<T>(w, h * 8 + j);
+    q[h] = mx_codes8(v, inv, s == 255u);
+  }
+  const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, LPU / 4, LPU);
+  const uint32_t s2 = __shfl_down_sync(0xffffffffu, s, LPU / 2, LPU);
+  const uint32_t s3 = __shfl_down_sync(0xffffffffu, s, LPU / 4 * 3, LPU);
+  if (!real) return;
+  const int blk = grp * 4 + l / (LPU / 4);
+  if (blk < blocks) {
+    uint8_t* dst = codes + (size_t)row * (size_t)blocks * 16 + grp * 64 + l * (EPL / 2);
+    if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = q[0];
+  }
+  if (tiled) {
+    if (l == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx_tiled_offset(row, grp, groups)) = s | (s1 << 8) | (s2 << 16) | (s3 << 24);
+  } else if (l % (LPU / 4) == 0 && blk < blocks) {
+    scales[(size_t)row * blocks + blk] = (uint8_t)s;
+  }
+}
+
 // Each group of lanes takes U units, all their loads issued before the first
-// is used; the unit's four scale bytes leave as one word.
+// is used.
 template <typename T, int VB, int U>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const uint8_t* __restrict__ x, int rows, int cols,
                                                                  long long stride_bytes,
@@ -190,45 +226,63 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const uint8_t* 
     load_share<T, VB>(x + (n ? (size_t)src * (size_t)stride_bytes : 0), grp[i] * kMxGroup + l * EPL, n, x, x_end, w[i]);
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const uint32_t s = mx_scale(share_amax<T>(w[i]));
-    const float inv = mx_inv_scale(s);
-    uint32_t q[EPL / 8];
-#pragma unroll
-    for (int h = 0; h < EPL / 8; ++h) {
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = share_value<T>(w[i], h * 8 + j);
-      q[h] = mx_codes8(v, inv, s == 255u);
+  for (int i = 0; i < U; ++i)
+    quantize_unit<T>(w[i], row[i], grp[i], u0 + (uint32_t)i * SUBS < units, cols, (int)groups.d, tiled, codes, scales);
+}
+
+// The gathered rows of a grouped product, one block a row.  Rows without a
+// source are zeros where a product reads them, inside an expert's tokens (row
+// r of expert e for offsets[e] <= r < offsets[e] + counts[e]); outside, where
+// most of a decoding step's rows lie (127 of padding an expert), nothing is
+// written.  Measured at 16 tokens, top-8 of 80 experts, 6144 columns (128 of
+// 10,368 rows real): see mxfp4_linear.
+constexpr int kMxRowThreads = 128;
+constexpr int kMxRowUnits = 3;
+template <typename T, int VB>
+__global__ void __launch_bounds__(kMxRowThreads) mx_quantize_rows_kernel(
+    const uint8_t* __restrict__ x, int rows, int cols, long long stride_bytes, const int32_t* __restrict__ perm,
+    const int32_t* __restrict__ offsets, const int32_t* __restrict__ counts, int E, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+  griddep_wait();
+  griddep_launch();
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>(), SUBS = kMxRowThreads / LPU;
+  const int row = blockIdx.x, src = __ldg(perm + row);
+  const bool live = src >= 0 && src < rows;
+  if (!live) {                                               // the same for the whole block
+    int before = 0;                                          // experts that start at or before the row
+    for (int e0 = 0; e0 < E; e0 += kMxRowThreads) {
+      const int e = e0 + (int)threadIdx.x;
+      before += __syncthreads_count(e < E && __ldg(offsets + e) <= row);
     }
-    const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, LPU / 4, LPU);
-    const uint32_t s2 = __shfl_down_sync(0xffffffffu, s, LPU / 2, LPU);
-    const uint32_t s3 = __shfl_down_sync(0xffffffffu, s, LPU / 4 * 3, LPU);
-    if (u0 + (uint32_t)i * SUBS < units) {
-      const int blk = grp[i] * 4 + l / (LPU / 4);
-      if (blk < blocks) {
-        uint8_t* dst = codes + (size_t)row[i] * (size_t)blocks * 16 + grp[i] * 64 + l * (EPL / 2);
-        if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
-        else *reinterpret_cast<uint32_t*>(dst) = q[0];
-      }
-      if (tiled) {
-        if (l == 0)
-          *reinterpret_cast<uint32_t*>(scales + mx_tiled_offset(row[i], grp[i], (int)groups.d)) =
-              s | (s1 << 8) | (s2 << 16) | (s3 << 24);
-      } else if (l % (LPU / 4) == 0 && blk < blocks) {
-        scales[(size_t)row[i] * blocks + blk] = (uint8_t)s;
-      }
+    if (before == 0 || row - __ldg(offsets + before - 1) >= __ldg(counts + before - 1)) return;
+  }
+  const int n = live ? cols : 0, groups = mx_groups(cols);
+  const int sub = threadIdx.x / LPU, l = threadIdx.x & (LPU - 1);
+  const uint8_t* x_end = x + (rows > 0 ? (size_t)(rows - 1) * (size_t)stride_bytes + (size_t)cols * T::size : 0);
+  const uint8_t* from = x + (live ? (size_t)src * (size_t)stride_bytes : 0);
+  for (int g0 = 0; g0 < groups; g0 += SUBS * kMxRowUnits) {
+    uint32_t w[kMxRowUnits][8];
+#pragma unroll
+    for (int i = 0; i < kMxRowUnits; ++i)
+      load_share<T, VB>(from, (g0 + i * SUBS + sub) * kMxGroup + l * EPL, n, x, x_end, w[i]);
+#pragma unroll
+    for (int i = 0; i < kMxRowUnits; ++i) {
+      const int grp = g0 + i * SUBS + sub;
+      quantize_unit<T>(w[i], row, grp, grp < groups, cols, groups, 1, codes, scales);
     }
   }
 }
 
-// The transpose: a thread owns C neighbouring columns over 64 rows of x, so
-// its two blocks of a column are 32 contiguous bytes of codes, a whole sector,
-// without a trip through shared memory.  A warp reads 32 C columns of a row at
-// once; the warps of a block cover consecutive rows, whose codes are
-// contiguous.
-constexpr int kMxTRows = 64;
+// The transpose: a thread owns C neighbouring columns (one word of a row) over
+// 32 rows of x, one block of each column, without a trip through shared
+// memory.  A warp reads 32 C columns of a row at once; the warps of a block
+// cover consecutive rows, whose codes are contiguous, so that the 16 bytes a
+// lane writes join their sector in L2.  64 rows a thread (whole sectors, twice
+// the registers) measured slower but at the largest size: 8192 x 6144 bf16
+// 29.0 us against 24.5, 4096 x 6144 16.3 against 12.7, 32768 x 6144 fp32 160
+// against 149, 65536 x 6144 bf16 191 against 199.
 constexpr int kMxTThreads = 128;
+constexpr int kMxTRows = kMxTThreads / 32 * kMxBlock;      // rows of x per block
 template <typename T, int C, bool WIDE>
 __global__ void __launch_bounds__(kMxTThreads) mx_quantize_t_kernel(const uint8_t* __restrict__ x, int rows, int cols,
                                                                     long long stride_bytes, int groups, int tiled,
@@ -239,50 +293,50 @@ __global__ void __launch_bounds__(kMxTThreads) mx_quantize_t_kernel(const uint8_
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * C;
-  const long long r0 = ((long long)blockIdx.y * (kMxTThreads / 32) + warp) * kMxTRows;
+  const long long r0 = ((long long)blockIdx.y * (kMxTThreads / 32) + warp) * kMxBlock;
   const int blocks = mx_blocks(rows);
   const long long r_end = tiled ? (long long)groups * kMxGroup : (long long)blocks * kMxBlock;
   if (r0 >= r_end) return;                                   // whole warps
   const uint8_t* p = x + (size_t)r0 * (size_t)stride_bytes + (size_t)c * T::size;
-  uint32_t w[kMxTRows];
+  uint32_t w[kMxBlock];
   if constexpr (WIDE) {
     if (c >= cols) return;
 #pragma unroll
-    for (int i = 0; i < kMxTRows; ++i)
+    for (int i = 0; i < kMxBlock; ++i)
       w[i] = r0 + i < rows ? __ldg(reinterpret_cast<const uint32_t*>(p + (size_t)i * (size_t)stride_bytes)) : 0u;
   } else {
     // Rows that are only 2-byte aligned: each lane reads the aligned word that
     // holds its first column, takes the word behind it from the next lane and
     // shifts the pair into place.  The word behind the last lane's is read by
-    // lane i for rows i and i + 32, so that no load sits in a branch.  Warps
+    // lane i for row i, so that no load sits in a branch.  Warps
     // whose words would reach past the matrix read element by element.
     const uint8_t* x_end = x + (size_t)(rows - 1) * (size_t)stride_bytes + (size_t)cols * 2;
-    const long long rl = min(r0 + kMxTRows, (long long)rows) - 1;
+    const long long rl = min(r0 + kMxBlock, (long long)rows) - 1;
     const uint8_t* first = p - (size_t)lane * 4;
     const uint8_t* last = x + (size_t)max(rl, 0ll) * (size_t)stride_bytes + (size_t)(c - lane * C) * 2 + 32 * 4;
     if (r0 < rows && first - 2 >= x && last + 4 <= x_end) {
-      const int n = (int)(rl + 1 - r0);                      // rows that exist: 64 but at the end
+      const int n = (int)(rl + 1 - r0);                      // rows that exist: 32 but at the end
       auto behind = [&](int i) -> uint32_t {
         const uint8_t* q = first + (size_t)min(i, n - 1) * (size_t)stride_bytes;
         return __ldg(reinterpret_cast<const uint32_t*>(q - (reinterpret_cast<uintptr_t>(q) & 2u)) + 32);
       };
-      const uint32_t next0 = behind(lane), next1 = behind(lane + 32);
+      const uint32_t behind_last = behind(lane);
 #pragma unroll
-      for (int i = 0; i < kMxTRows; ++i) {
+      for (int i = 0; i < kMxBlock; ++i) {
         const uint8_t* q = p + (size_t)i * (size_t)stride_bytes;
         w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t*>(q - (reinterpret_cast<uintptr_t>(q) & 2u))) : 0u;
       }
 #pragma unroll
-      for (int i = 0; i < kMxTRows; ++i) {
+      for (int i = 0; i < kMxBlock; ++i) {
         const uint8_t* q = p + (size_t)i * (size_t)stride_bytes;
         const uint32_t other = __shfl_down_sync(0xffffffffu, w[i], 1);
-        const uint32_t next = __shfl_sync(0xffffffffu, i < 32 ? next0 : next1, i & 31);
+        const uint32_t next = __shfl_sync(0xffffffffu, behind_last, i);
         const uint32_t pair = __funnelshift_r(w[i], lane == 31 ? next : other, (uint32_t)(reinterpret_cast<uintptr_t>(q) & 2u) * 8u);
         w[i] = i < n ? pair : 0u;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kMxTRows; ++i) {
+      for (int i = 0; i < kMxBlock; ++i) {
         const uint16_t* q = reinterpret_cast<const uint16_t*>(p + (size_t)i * (size_t)stride_bytes);
         const bool in = r0 + i < rows;
         const uint32_t a = in && c < cols ? __ldg(q) : 0u, b = in && c + 1 < cols ? __ldg(q + 1) : 0u;
@@ -291,55 +345,38 @@ __global__ void __launch_bounds__(kMxTThreads) mx_quantize_t_kernel(const uint8_
     }
     if (c >= cols) return;
   }
-  const int blk = (int)(r0 / kMxBlock);                      // even: the pair stays inside a group
+  const int blk = (int)(r0 / kMxBlock);
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    uint32_t sc[2], q[2][4];
+    uint32_t m = 0u;
+    if constexpr (T::size == 2) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      auto val = [&](int i) -> float {
-        const uint32_t b = w[h * 32 + i];
-        if constexpr (T::size == 4) return __uint_as_float(b);
-        else return j ? T::hi(b) : T::lo(b);
-      };
-      uint32_t m;
-      if constexpr (T::size == 2) {
-        m = 0u;
+      for (int i = 0; i < kMxBlock; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      m = T::mag(j ? m >> 16 : m & 0xFFFFu);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m = __vmaxu2(m, w[h * 32 + i] & 0x7FFF7FFFu);
-        m = T::mag(j ? m >> 16 : m & 0xFFFFu);
-      } else {
-        m = 0u;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = max(m, w[h * 32 + i] & 0x7FFFFFFFu);
-      }
-      const uint32_t s = sc[h] = mx_scale(m);
-      const float inv = mx_inv_scale(s);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = val(g * 8 + i);
-        q[h][g] = mx_codes8(v, inv, s == 255u);
-      }
+      for (int i = 0; i < kMxBlock; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
     }
-    if (c + j < cols) {
-      uint8_t* d = codes + ((size_t)(c + j) * blocks + blk) * 16;
-      if ((blocks & 1) == 0 && blk < blocks) {               // both blocks exist and the pair is 32-byte aligned
-        store_words8<32>(d, &q[0][0]);
-      } else {
-        if (blk < blocks) *reinterpret_cast<uint4*>(d) = make_uint4(q[0][0], q[0][1], q[0][2], q[0][3]);
-        if (blk + 1 < blocks) *reinterpret_cast<uint4*>(d + 16) = make_uint4(q[1][0], q[1][1], q[1][2], q[1][3]);
+    const uint32_t s = mx_scale(m);
+    const float inv = mx_inv_scale(s);
+    uint32_t q[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = w[g * 8 + i];
+        if constexpr (T::size == 4) v[i] = __uint_as_float(b);
+        else v[i] = j ? T::hi(b) : T::lo(b);
       }
-      if (tiled) {
-        *reinterpret_cast<uint16_t*>(scales + mx_tiled_offset(c + j, blk >> 2, groups) + (blk & 3)) =
-            (uint16_t)(sc[0] | (sc[1] << 8));
-      } else {
-        uint8_t* e = scales + (size_t)(c + j) * blocks + blk;
-        if (blk < blocks) e[0] = (uint8_t)sc[0];
-        if (blk + 1 < blocks) e[1] = (uint8_t)sc[1];
-      }
+      q[g] = mx_codes8(v, inv, s == 255u);
     }
+    if (c + j >= cols) continue;
+    if (blk < blocks)
+      *reinterpret_cast<uint4*>(codes + ((size_t)(c + j) * blocks + blk) * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+    // (tiled: the padding blocks of the last group get scale 0, as no row exists)
+    if (tiled) scales[mx_tiled_offset(c + j, blk >> 2, groups) + (blk & 3)] = (uint8_t)s;
+    else if (blk < blocks) scales[(size_t)(c + j) * blocks + blk] = (uint8_t)s;
   }
 }
 
@@ -482,7 +519,7 @@ static nvfp4_status count_units(const char* name, int rows, int cols, uint32_t* 
 
 nvfp4_status launch_mx_quantize(const void* x, int dtype, int rows, int cols, long long row_stride,
                                 const int32_t* perm, int out_rows, int layout, uint8_t* codes, uint8_t* scales,
-                                cudaStream_t s) {
+                                cudaStream_t s, const int32_t* expert_offsets, const int32_t* expert_counts, int E) {
   uint32_t units = 0;
   NV_CHECK(count_units("mxfp4_quantize", out_rows, cols, &units));
   int sms = 0;
@@ -498,6 +535,10 @@ nvfp4_status launch_mx_quantize(const void* x, int dtype, int rows, int cols, lo
     const dim3 grid((units + per_block - 1) / per_block);
     return with_width<T>(row_access_bytes(x, rows > 1 ? sb : 0, T::size), [&](auto vb) -> nvfp4_status {
       constexpr int VB = decltype(vb)::value;
+      if (perm && expert_counts && out_rows < 2ll * 127 * E)
+        return launch_dependent("mx_quantize_rows_kernel", mx_quantize_rows_kernel<T, VB>, dim3((unsigned)out_rows),
+                                dim3(kMxRowThreads), 0, s, xb, rows, cols, sb, perm, expert_offsets, expert_counts, E,
+                                codes, scales);
       return launch_dependent("mx_quantize_kernel",
                               many ? mx_quantize_kernel<T, VB, kMxUnits> : mx_quantize_kernel<T, VB, 1>, grid,
                               dim3(kMxThreads), 0, s, xb, rows, cols, sb, perm, units, groups, tiled, codes, scales);
@@ -534,13 +575,11 @@ extern "C" nvfp4_status mxfp4_quantize_transposed(const void* x, int dtype, int 
   NV_CHECK(check_mx_source("mxfp4_quantize_transposed", x, dtype, rows, cols, row_stride));
   NV_REQUIRE(rows >= 1, NVFP4_ERR_INVALID_ARG, "mxfp4_quantize_transposed: rows=%d (the result's columns)", rows);
   NV_CHECK(check_mx_quantized("mxfp4_quantize_transposed", codes, scales, layout));
-  constexpr int per_block = kMxTThreads / 32 * kMxTRows;
-  NV_REQUIRE(rows <= 65535 * per_block, NVFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_quantize_transposed: rows=%d is above %d",
-             rows, 65535 * per_block);
+  NV_REQUIRE(rows <= 65535 * kMxTRows, NVFP4_ERR_UNSUPPORTED_SHAPE, "mxfp4_quantize_transposed: rows=%d is above %d",
+             rows, 65535 * kMxTRows);
   int sms = 0;
   NV_CHECK(device_sm_count(&sms));
   const int groups = mx_groups(rows), tiled = layout == NVFP4_LAYOUT_TILED;
-  const int gy = (groups * kMxGroup + per_block - 1) / per_block;
   const uint8_t* xb = static_cast<const uint8_t*>(x);
   cudaStream_t s = as_stream(stream);
   return with_type(dtype, [&](auto tag) -> nvfp4_status {
@@ -550,7 +589,8 @@ extern "C" nvfp4_status mxfp4_quantize_transposed(const void* x, int dtype, int 
     // one word a thread and row: needs 4-byte aligned rows and, for pairs, a
     // second column in the last pair
     const bool wide = row_access_bytes(x, rows > 1 ? sb : 0, T::size) >= 4 && cols % C == 0;
-    const dim3 grid((unsigned)((cols + 32ll * C - 1) / (32 * C)), gy);
+    const dim3 grid((unsigned)((cols + 32ll * C - 1) / (32 * C)),
+                    (unsigned)((groups * kMxGroup + kMxTRows - 1) / kMxTRows));
     if constexpr (C == 2) {
       if (!wide)
         return launch_dependent("mx_quantize_t_kernel", mx_quantize_t_kernel<T, C, false>, grid, dim3(kMxTThreads), 0,

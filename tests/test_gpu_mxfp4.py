@@ -183,7 +183,7 @@ MNK = [(1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16,
        (128, 128, 512), (129, 255, 320), (200, 1024, 640), (256, 256, 256), (257, 130, 224), (300, 700, 384),
        (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000),
        # on CTA pairs (tests/test_mxfp4.py checks that these sizes reach them), K ending with one atom and two
-       (1536, 4096, 96), (1500, 3999, 300), (3000, 2049, 416)]
+       (1536, 4096, 1312), (1500, 3999, 1400), (3000, 2049, 1700)]
 
 
 @pytest.mark.parametrize("M,N,K", MNK)
@@ -221,7 +221,7 @@ def test_matmul_bias_row_weight_and_strided_out():
     require_cuda()
     c = capi()
     rng = np.random.default_rng(5)
-    for M, N, K in [(3, 200, 320), (3, 200, 2048), (40, 130, 96), (300, 300, 256), (1500, 3999, 300)]:
+    for M, N, K in [(3, 200, 320), (3, 200, 2048), (40, 130, 96), (300, 300, 256), (1500, 3999, 1400)]:
         a, av = operand(M, K, 1)
         b, bv = operand(N, K, 2)
         bias = rng.standard_normal(N).astype(np.float32)
@@ -239,16 +239,16 @@ def test_matmul_bias_row_weight_and_strided_out():
 def test_a_nan_block_reaches_its_row_only(M):
     require_cuda()
     c = capi()
-    a, av = operand(M, 300, 3)
-    N = 200 if M < 1500 else 3999
-    b, bv = operand(N, 300, 4)
+    N, K = (200, 300) if M < 1500 else (3999, 1420)
+    a, av = operand(M, K, 3)
+    b, bv = operand(N, K, 4)
     clean = c.mxfp4_matmul(a, b)
-    at = int(mxfp4.tiled_index(M, 300)[M - 1, 9])              # the last, partly filled block
+    at = int(mxfp4.tiled_index(M, K)[M - 1, K // 32])          # the last, partly filled block
     a.scales[at] = 255
     y = c.mxfp4_matmul(a, b)
     assert torch.isnan(y[M - 1]).all() and torch.equal(y[:M - 1], clean[:M - 1])
     a.scales[at] = 127
-    b.scales[int(mxfp4.tiled_index(N, 300)[131, 0])] = 255
+    b.scales[int(mxfp4.tiled_index(N, K)[131, 0])] = 255
     y = c.mxfp4_matmul(a, b)
     assert torch.isnan(y[:, 131]).all() and not torch.isnan(y[:, :131]).any() and not torch.isnan(y[:, 132:]).any()
 
@@ -257,7 +257,7 @@ def test_padding_bytes_do_not_matter():
     """Scale bytes of padding rows may hold anything, NaN included."""
     require_cuda()
     c = capi()
-    for M, N, K in [(3, 70, 100), (150, 260, 300), (1500, 3999, 300)]:
+    for M, N, K in [(3, 70, 100), (150, 260, 300), (1500, 3999, 1400)]:
         a, av = operand(M, K, 8)
         b, bv = operand(N, K, 9)
         want = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
@@ -284,8 +284,8 @@ def grouped_case(counts, gaps, N, K, seed):
     ([3] * 40, [0] * 40, 128, 512),
     ([1000, 0, 257], [0, 0, 0], 384, 160),
     ([0, 0, 0], [0, 1, 0], 128, 96),
-    ([1000, 0, 385, 2900], [0, 0, 0, 0], 2048, 288),        # on CTA pairs
-    ([1500, 1024, 1, 2000], [0, 0, 1, 0], 1920, 160),        # pairs, an odd number of 128-row b tiles per expert
+    ([1500, 0, 385, 3500], [0, 0, 0, 0], 2048, 1312),        # on CTA pairs
+    ([1500, 1536, 1, 2900], [0, 0, 0, 0], 1920, 1440),        # pairs, an odd number of 128-row b tiles per expert
 ])
 def test_grouped_matmul(counts, gaps, N, K):
     require_cuda()
@@ -338,10 +338,41 @@ def test_linear_is_quantize_then_matmul():
         assert not yp[perm < 0].any()
 
 
+@pytest.mark.parametrize("with_counts", [True, False])
+def test_grouped_linear_with_padding_rows(with_counts):
+    """Rows of perm without a source: inside an expert's tokens they are
+    zeros (y = weight * bias); outside them nothing is read or written."""
+    require_cuda()
+    c = capi()
+    E, N, K = 3, 128, 330
+    off = torch.tensor([0, 256, 256, 512], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([130, 0, 7], dtype=torch.int32, device="cuda")
+    x = matrix(50, K, torch.bfloat16, special=False).cuda()
+    w, _ = operand(E * N, K, 4)
+    perm = torch.full((512,), -1, dtype=torch.int32)
+    perm[:130] = torch.arange(130) % 50
+    perm[256:263] = torch.arange(7)
+    perm[3] = perm[129] = perm[260] = -1
+    perm = perm.cuda()
+    rw = torch.randn(512, device="cuda")
+    bias = torch.randn(E * N, device="cuda")
+    out = torch.full((512, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((c.mxfp4_linear_workspace_size(512, K),), 255, dtype=torch.uint8, device="cuda")   # NaN scales
+    kw = dict(row_weight=rw, bias=bias, expert_offsets=off, expert_counts=cnt if with_counts else None)
+    c.mxfp4_linear(x, w, perm=perm, out=out, workspace=ws, **kw)
+    want = torch.full_like(out, 9.0)
+    c.mxfp4_matmul(c.mxfp4_quantize(x, perm=perm), w, out=want, **kw)
+    assert torch.equal(out, want) and torch.isfinite(out).all()
+    if with_counts:
+        assert (out[130:256] == 9.0).all() and (out[263:] == 9.0).all()
+    for r, e in ((3, 0), (129, 0), (260, 2)):
+        assert torch.equal(out[r], (rw[r] * bias[e * N:(e + 1) * N]).to(torch.bfloat16))
+
+
 def test_results_do_not_change_from_run_to_run():
     require_cuda()
     c = capi()
-    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024), (1536, 4096, 96)]:
+    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024), (1536, 4096, 1312)]:
         a, _ = operand(M, K, 1)
         b, _ = operand(N, K, 2)
         first = c.mxfp4_matmul(a, b, out_dtype=torch.float32)

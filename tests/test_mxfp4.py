@@ -176,9 +176,10 @@ def test_product_plans():
                         assert stages * stage + (3 * E + 1) * 4 + 1024 <= 227 * 1024 - 256
     assert plan(1, 6144, 512)[1] == 1 and plan(16, 128, 6144)[1] == 4 and plan(100, 300, 2048)[1] == 4
     assert plan(1, 1000, 4096) == (16, 4, False, 5)
-    for M, N, K in ((1536, 4096, 96), (1500, 3999, 300), (3000, 2049, 416)):
+    for M, N, K in ((1536, 4096, 1312), (1500, 3999, 1400), (1500, 3999, 1420), (3000, 2049, 1700)):
         assert plan(M, N, K)[2]
-    assert plan(4480, 2048, 288, 4)[2] and plan(4864, 1920, 160, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
+    assert plan(5632, 2048, 1312, 4)[2] and plan(6144, 1920, 1440, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
+    assert plan(256, 256, 256)[0] == 128 and plan(1024, 4096, 6144)[0] == 256
     with pytest.raises(ValueError):
         plan(0, 1, 1)
 
