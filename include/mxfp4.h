@@ -30,7 +30,9 @@
  *
  * Conventions are those of nvfp4_moe.h (device memory of the caller, nothing
  * allocated, work queued on `stream`, checks on the host before anything is
- * queued).  Sizes of zero rows are legal and queue nothing.
+ * queued).  A workspace serves one call at a time: calls or captured graphs
+ * that share one run one after the other.  Sizes of zero rows are legal and
+ * queue nothing.
  */
 #ifndef NVFP4_MOE_MXFP4_H
 #define NVFP4_MOE_MXFP4_H
@@ -98,7 +100,8 @@ NVFP4_API nvfp4_status mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_sca
 
 /* The product with a = x (or x[perm]) quantised in the call: mxfp4_quantize
  * into the workspace, then mxfp4_matmul on its M rows (M = perm_rows with
- * perm, else rows).  The workspace's status word is that of the product. */
+ * perm, else rows).  The workspace's status word is that of the product.  y
+ * may take the place of x. */
 NVFP4_API size_t mxfp4_linear_workspace_size(int M, int K);
 NVFP4_API nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long long row_stride, const int32_t* perm,
                                     int perm_rows, const uint8_t* b_codes, const uint8_t* b_scales, int N, int K,

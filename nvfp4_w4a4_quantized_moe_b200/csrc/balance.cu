@@ -616,6 +616,8 @@ extern "C" nvfp4_status moe_balance_loss_backward(const void* logits, int dtype,
   if (T == 0) return NVFP4_OK;
   NV_REQUIRE(counts && tokens && grad_loss && dlogits, NVFP4_ERR_INVALID_ARG,
              "moe_balance_loss_backward: a required pointer is NULL");
+  NV_REQUIRE(dlogits != logits, NVFP4_ERR_INVALID_ARG,
+             "moe_balance_loss_backward: dlogits may not take the place of logits");
   NV_REQUIRE(T <= 1 || grad_stride >= E, NVFP4_ERR_INVALID_ARG,
              "moe_balance_loss_backward: gradient stride %lld is below E=%d", grad_stride, E);
   NV_REQUIRE(aligned(dlogits, mx_elem_size(dtype)) && aligned(counts, 4) && aligned(tokens, 4) &&

@@ -178,7 +178,7 @@ def product_bound(a, b, ref, dtype, row_weight=None, bias=None):
     return err + fi.eps / 2 * (np.abs(ref) + err) + fi.smallest_normal * fi.eps
 
 
-MNK = [(1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16, 256, 128), (17, 500, 160),
+MNK = [(3, 5, 1), (1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16, 256, 128), (17, 500, 160),
        (31, 64, 256), (32, 129, 288), (33, 1000, 544), (64, 384, 1024), (65, 128, 100), (100, 300, 2048),
        (128, 128, 512), (129, 255, 320), (200, 1024, 640), (256, 256, 256), (257, 130, 224), (300, 700, 384),
        (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000),
@@ -378,6 +378,105 @@ def test_results_do_not_change_from_run_to_run():
         first = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
         for _ in range(5):
             assert torch.equal(c.mxfp4_matmul(a, b, out_dtype=torch.float32), first)
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 bytes: the last rows come out as they do by
+    themselves."""
+    require_cuda()
+    c = capi()
+    rows, cols = 66000, 33000                                  # 8.7 GB of fp32
+    x = torch.empty(rows, cols, device="cuda")
+    tail = matrix(300, cols, torch.float32, special=False).cuda()
+    x[:-300] = 0.0
+    x[-300:] = tail
+    q, qt = c.mxfp4_quantize(x, "canonical"), c.mxfp4_quantize(tail, "canonical")
+    assert torch.equal(q.codes[-300:], qt.codes) and torch.equal(q.scales[-300:], qt.scales)
+    assert not q.codes[:-300].any() and not q.scales[:-300].any()
+    back = c.mxfp4_dequantize(q, dtype=torch.float32, out=x)
+    assert torch.equal(back[-300:], c.mxfp4_dequantize(qt, dtype=torch.float32)) and not back[:1000].any()
+    wide = c.mxfp4_quantize_transposed(back[:, -40:], "canonical")       # rows 33000 apart, past 2^32 bytes
+    alone = c.mxfp4_quantize_transposed(back[:, -40:].contiguous(), "canonical")
+    assert torch.equal(wide.codes, alone.codes) and torch.equal(wide.scales, alone.scales)
+    del x, back, q, wide, alone
+    M, N, K = 40000, 60000, 64                                 # 4.8 GB of bf16 outputs
+    a, _ = operand(M, K, 1)
+    b, _ = operand(N, K, 2)
+    y = c.mxfp4_matmul(a, b)
+    ac, bc = c.mxfp4_dequantize(a), c.mxfp4_dequantize(b)
+    part = c.mxfp4_matmul(c.mxfp4_quantize(ac[-700:].contiguous()), c.mxfp4_quantize(bc[-900:].contiguous()))
+    assert torch.equal(y[-700:, -900:], part)
+
+
+def test_y_may_take_the_place_of_x():
+    require_cuda()
+    c = capi()
+    for M in (5, 600):
+        x = matrix(M, 512, torch.bfloat16, special=False).cuda()
+        w, _ = operand(512, 512, 3)
+        want = c.mxfp4_linear(x, w)
+        assert torch.equal(c.mxfp4_linear(x, w, out=x), want)
+
+
+FIRST_CALLS_IN_A_CAPTURE = """
+import sys, torch
+sys.path.insert(0, %r)
+from nvfp4_w4a4_quantized_moe_b200 import capi as c
+torch.manual_seed(0)
+x = [torch.randn(m, 640, device="cuda").bfloat16() for m in (1, 300, 1536)]
+w = torch.randn(4096, 640, device="cuda").bfloat16()
+l = torch.randn(3000, 64, device="cuda")
+idx = l.topk(4).indices.int()
+one = torch.ones(1, device="cuda")
+def everything():
+    q = c.mxfp4_quantize(w)
+    t = c.mxfp4_quantize_transposed(w)
+    b = c.moe_balance_loss(l, idx, 0.1)
+    return ([c.mxfp4_linear(v, q) for v in x] + [c.mxfp4_dequantize(t), b.loss, b.probs,
+            c.moe_balance_loss_backward(l, b, one), c.moe_balance_loss(l[:9], idx[:9], 0.1).loss])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = everything()
+g.replay()
+torch.cuda.synchronize()
+want = everything()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    require_cuda()
+    import subprocess
+    import sys
+
+    from _util import ROOT
+    capi()
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_IN_A_CAPTURE % ROOT], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_calls_from_two_threads_and_streams():
+    require_cuda()
+    c = capi()
+    import threading
+    w, _ = operand(1000, 640, 1)
+    xs = [matrix(m, 640, torch.bfloat16, special=False).cuda() for m in (3, 300)]
+    want = [c.mxfp4_linear(x, w) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                if not torch.equal(c.mxfp4_linear(xs[i], w), want[i]):
+                    bad.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1, 0, 1)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad
 
 
 def test_side_stream_and_captured_graphs_sharing_a_workspace():

@@ -195,8 +195,11 @@ def test_balance_refusals():
     assert f(E=0) == 2 and f(E=1025, st=1025) == 2 and f(k=0) == 2 and f(k=33) == 2
     assert f(n=256) == 5 and f(ws=None) == 5
 
-    def b(T=4, E=8, gs=8, d=FAKE, g=FAKE):
+    other = ctypes.c_void_p(0x2000)
+
+    def b(T=4, E=8, gs=8, d=other, g=FAKE):
         return lib.moe_balance_loss_backward(FAKE, 2, T, E, 8, 2, 0, None, None, 1, 0.1, FAKE, FAKE, g, d, gs, None)
+    assert b(d=FAKE) == 1 and b"place" in lib.nvfp4_last_error()
     assert b(gs=7) == 1 and b(d=None) == 1 and b(g=None) == 1 and b(E=2000) == 2 and b(T=0) == 0
     c = capi()
     assert c.moe_balance_loss_workspace_size(0, 8) > 0 and c.moe_balance_loss_workspace_size(4, 0) == 0
