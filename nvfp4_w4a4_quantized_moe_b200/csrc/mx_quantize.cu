@@ -43,54 +43,65 @@ template <typename T> __host__ __device__ constexpr int block_subs() { return kM
 constexpr bool is_narrow(int vb) { return vb < 16; }
 constexpr int kMxWarpBytes = 1024;
 
-// The row and column that byte `b` of the warp's units belongs to.
-struct UnitPlace {
-  int row, col;
-};
-template <typename T>
-NVDEV UnitPlace place_of(const FastDiv& groups, uint32_t units, uint32_t first, int b) {
-  constexpr int unit_bytes = kMxGroup * T::size;
-  const uint32_t u = min(first + (uint32_t)(b / unit_bytes), units - 1);
-  UnitPlace p;
-  p.row = (int)groups.quotient(u);
-  p.col = (int)(u - (uint32_t)p.row * groups.d) * kMxGroup + (b % unit_bytes) / T::size;
-  return p;
-}
 template <int VB> struct Narrow;
 template <> struct Narrow<8> { using type = uint2; };
 template <> struct Narrow<4> { using type = uint32_t; };
-template <> struct Narrow<2> { using type = uint16_t; };
 
+// Writes the warp's units, a lane's share of which is `w`: unit by unit, with
+// neighbouring lanes on neighbouring words.  row, grp: the lane's own unit.
 template <typename T, int VB>
-NVDEV void store_staged(uint8_t* out, int cols, long long stride_bytes, const FastDiv& groups, uint32_t units,
-                        uint32_t first, uint8_t* buf, const uint32_t* w) {
-  using V = typename Narrow<VB>::type;
-  constexpr int per = VB / T::size, unit_bytes = kMxGroup * T::size;
+NVDEV void store_staged(uint8_t* out, int cols, long long stride_bytes, int row, int grp, bool real, uint8_t* buf,
+                        const uint32_t* w) {
+  constexpr int LPU = unit_lanes<T>(), unit_bytes = kMxGroup * T::size;
   const int lane = threadIdx.x & 31;
-  __syncwarp();
+  __syncwarp();                                              // the previous units have left buf
   uint4* mine = reinterpret_cast<uint4*>(buf + lane * 32);
   mine[0] = make_uint4(w[0], w[1], w[2], w[3]);
   mine[1] = make_uint4(w[4], w[5], w[6], w[7]);
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 32 / VB; ++j) {
-    const int b = (j * 32 + lane) * VB;
-    if (first + (uint32_t)(b / unit_bytes) >= units) continue;
-    const UnitPlace p = place_of<T>(groups, units, first, b);
-    uint8_t* at = out + (size_t)p.row * (size_t)stride_bytes + (size_t)p.col * T::size;
-    if (p.col + per <= cols) {
-      *reinterpret_cast<V*>(at) = reinterpret_cast<const V*>(buf)[j * 32 + lane];
-    } else {
+  for (int unit = 0; unit < 32 / LPU; ++unit) {
+    const int r = __shfl_sync(0xffffffffu, row, unit * LPU), g = __shfl_sync(0xffffffffu, grp, unit * LPU);
+    if (!__shfl_sync(0xffffffffu, (int)real, unit * LPU)) continue;
+    const uint8_t* from = buf + unit * unit_bytes;
+    uint8_t* to = out + (size_t)r * (size_t)stride_bytes + (size_t)g * unit_bytes;
+    const int n = min(kMxGroup, cols - g * kMxGroup);        // elements of the unit
+    if constexpr (VB == 2) {
+      // rows of 2-byte elements at any of them: words from the first aligned
+      // one on, the ends by themselves
+      const int mis = (int)(reinterpret_cast<uintptr_t>(to) >> 1) & 1;
+      const uint16_t* f = reinterpret_cast<const uint16_t*>(from);
+      uint16_t* t = reinterpret_cast<uint16_t*>(to);
 #pragma unroll
-      for (int e = 0; e < per; ++e)
-        if (p.col + e < cols) {
-          if constexpr (T::size == 2) reinterpret_cast<uint16_t*>(at)[e] = reinterpret_cast<const uint16_t*>(buf + b)[e];
-          else reinterpret_cast<uint32_t*>(at)[e] = reinterpret_cast<const uint32_t*>(buf + b)[e];
+      for (int it = 0; it < 2; ++it) {
+        const int e = 2 * (it * 32 + lane) + mis;
+        if (e + 1 < n) {
+          *reinterpret_cast<uint32_t*>(t + e) = (uint32_t)f[e] | ((uint32_t)f[e + 1] << 16);
+        } else if (e < n) {
+          t[e] = f[e];
         }
+      }
+      if (mis && lane == 0) t[0] = f[0];
+    } else {
+      using V = typename Narrow<VB>::type;
+      constexpr int per = VB / T::size;                      // elements per access
+#pragma unroll
+      for (int it = 0; it < unit_bytes / (32 * VB); ++it) {
+        const int i = it * 32 + lane, e = i * per;
+        if (e + per <= n) {
+          reinterpret_cast<V*>(to)[i] = reinterpret_cast<const V*>(from)[i];
+        } else {
+#pragma unroll
+          for (int j = 0; j < per; ++j)
+            if (e + j < n) {
+              if constexpr (T::size == 2) reinterpret_cast<uint16_t*>(to)[e + j] = reinterpret_cast<const uint16_t*>(from)[e + j];
+              else reinterpret_cast<uint32_t*>(to)[e + j] = reinterpret_cast<const uint32_t*>(from)[e + j];
+            }
+        }
+      }
     }
   }
 }
-
 // Elements at or past `n` read as 0.  `lo` and `hi` bound the matrix's bytes:
 // the aligned pieces of a narrow row may reach into its neighbours, not past
 // the matrix.
@@ -442,8 +453,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const uint8_t
       else w[j] = __float_as_uint(v[j]);
     }
     if constexpr (is_narrow(VB)) {
-      store_staged<T, VB>(out, cols, stride_bytes, groups, units,
-                          u0 - (threadIdx.x & 31) / LPU + (uint32_t)i * SUBS, warp_buf[threadIdx.x >> 5], w);
+      store_staged<T, VB>(out, cols, stride_bytes, row[i], grp[i], u0 + (uint32_t)i * SUBS < units,
+                          warp_buf[threadIdx.x >> 5], w);
     } else {
       const int c = grp[i] * kMxGroup + l * EPL;
       if (u0 + (uint32_t)i * SUBS >= units || c >= cols) continue;
