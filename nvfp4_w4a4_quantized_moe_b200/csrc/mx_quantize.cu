@@ -29,17 +29,21 @@ template <typename T> __host__ __device__ constexpr int unit_lanes() { return kM
 template <typename T> __host__ __device__ constexpr int block_subs() { return kMxThreads / unit_lanes<T>(); }
 
 // Rows that allow only narrow accesses (8 bytes or less).
-//   Reading 16-bit elements that are only 2-byte aligned: a lane's 32 bytes lie
-//   inside three aligned 16-byte pieces; it reads those and shifts them into
-//   place.  4- and 8-byte accesses are left as they are (L1 serves the
-//   neighbours' share of a line).
+//   Reading rows that are 2- or 4-byte aligned: a lane's 32 bytes lie inside
+//   three aligned 16-byte pieces; it reads those and shifts them into place.
+//   8-byte accesses are left as they are (L1 serves the neighbours' share of a
+//   line).
 //   Writing: the warp's consecutive units (1 KiB in all) go through shared
-//   memory, so that neighbouring lanes write neighbouring accesses instead of
-//   4 to 16 accesses 32 bytes apart each.
-// Measured (one B200): 16384 x 6145 bf16, 2-byte rows: reading element by
-// element 107 us, through shared memory 118 us, shifted 66 us; writing element
-// by element 544 us, staged 80 us.  8191 x 6100 fp16, 8-byte rows: reading as
-// it is 25 us, shifted 35 us; writing as it is 53 us, staged 30 us.
+//   memory, so that neighbouring lanes write neighbouring words instead of 4
+//   to 16 accesses 32 bytes apart each.
+// Measured (one B200, us; quantise reads x, read-back writes it):
+//                                   one by one   through shared   shifted
+//   read  16384 x 6145 bf16 (2 B)      107            127           59
+//   read  16384 x 6146 bf16 (4 B)       61             72           59
+//   read  8192 x 6145 fp32 (4 B)        58             58           50
+//   read  8191 x 6100 fp16 (8 B)        23             31           35
+//   write 16384 x 6145 bf16 (2 B)      544             68
+//   write 8191 x 6100 fp16 (8 B)        53             27
 constexpr bool is_narrow(int vb) { return vb < 16; }
 constexpr int kMxWarpBytes = 1024;
 
@@ -110,7 +114,7 @@ NVDEV void load_share(const uint8_t* row, int c, int n, const uint8_t* lo, const
   constexpr int EPL = lane_elems<T>();
   if (c + EPL <= n) {
     const uint8_t* at = row + (size_t)c * T::size;
-    if constexpr (VB >= 4) {
+    if constexpr (VB >= 8) {
       load_words8<VB>(at, w);
       return;
     } else {
