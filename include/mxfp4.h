@@ -88,8 +88,8 @@ NVFP4_API nvfp4_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* sca
  * held.  Dense: E = 0 and expert_offsets = expert_counts = NULL; every row is
  * written.
  *
- * a codes, b codes and scales need 16-byte alignment.  E <= 1024.  The
- * result does not depend on scheduling.
+ * a codes, b codes and scales need 16-byte alignment.  E <= 1024, M, N and K
+ * <= 2^30.  The result does not depend on scheduling.
  * ---------------------------------------------------------------------- */
 NVFP4_API size_t mxfp4_matmul_workspace_size(void);
 NVFP4_API nvfp4_status mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_scales, int M, const uint8_t* b_codes,

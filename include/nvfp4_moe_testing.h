@@ -98,7 +98,7 @@ NVFP4_API int nvfp4_test_router_splits(int T, int H, int* stages_per_split);
  * (mxfp4_matmul with these sizes on 148 SMs), with the K splits in *splits, 1
  * or 0 in *pair for tiles on CTA pairs, and the pipeline stages in *stages
  * (each nullable).  The order of the fp32 sums follows the splits.  Returns -1
- * for M < 1, N < 1, K < 1 or E < 0. */
+ * for sizes that mxfp4_matmul refuses. */
 NVFP4_API int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages);
 
 #ifdef __cplusplus

@@ -14,7 +14,14 @@
 // of the row's sequence held in registers while the sequence lasts.
 //
 // Bound: HBM (logits in; gradient out), with one exponential (softmax) or one
-// exponential and one reciprocal (sigmoid) per element close behind.
+// exponential and one reciprocal (sigmoid) per element behind it; below some
+// ten thousand tokens the chain of loads, joins and launches.  Measured on one
+// B200 (fp32, 128 experts, top-8): 262,144 tokens forward 38 us (3.7 TB/s),
+// backward 50 us (5.3 TB/s); 65,536 tokens 19 and 14 us (inputs in L2); 16
+// tokens of 80 experts 3.8 and 2.7 us.  With four logits a lane and row instead of
+// sixteen (five shuffles for each maximum and sum), a reciprocal a logit for
+// softmax too and the choices counted before the rows, 65,536 tokens took 57
+// and 31 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -488,6 +495,9 @@ static inline int balance_chunk(int T, int E) {
   return std::max(1, (int)(((long long)T + 148ll * 3 * step - 1) / (148ll * 3 * step))) * step;
 }
 // Few logits: one block does the whole forward, one launch instead of two.
+// Measured, one block against two kernels (us): 16 x 80 3.7 and 8.8, 64 x 80
+// 4.1 and 8.9, 128 x 128 6.3 and 9.5, 256 x 128 9.4 and 9.6, 512 x 128 15.5
+// and 9.5.  It walks its sequences one after the other, hence at most 64.
 static inline bool balance_one_block(int T, int E, int S) { return (long long)T * E <= kBalOneBlock && S <= 64; }
 
 struct BalanceScratch {

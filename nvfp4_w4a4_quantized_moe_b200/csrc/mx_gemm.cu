@@ -3,9 +3,10 @@
 // grouped by expert.
 //
 // The block scales are applied inside the MMA (kind::mxf4, scale_vec::2X: two
-// E8M0 bytes per row and 64-element step), the products of E2M1 values under
-// powers of two are exact and accumulate in fp32, so the one rounding that
-// the definition has is the store.
+// E8M0 bytes per row and 64-element step): products of E2M1 values under powers
+// of two are exact, their sums fp32 (operands with a common scale sum exactly
+// up to 2^24 units), bias and row weight one fp32 operation each, and the
+// store rounds to the output type.
 //
 // Orientation: the 128 rows of an MMA tile (the tensor-memory lanes) are rows
 // of b, its N columns are rows of a ("tokens").  A decoding step's few tokens
@@ -23,6 +24,22 @@
 // rank r adds the columns r, r + S, ... of all of them in rank order and
 // stores them, so the result does not depend on scheduling and takes no
 // second kernel and no workspace.
+//
+// Bound: many tokens by the tensor pipe (the power-capped clock included) and
+// by how fast L2 feeds the SMs, few tokens by HBM reading b, a single small
+// product by the chain launch, TMA, MMA, join, store.  Measured on one B200,
+// bf16 outputs, in a stream of calls:
+//   8192 x 4096 x 6144   72 us, 5.7 PFLOP/s (0.86 of four times the measured
+//                        bf16 rate)
+//   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 8.6
+//   16 x 6144 x 6144     6.8 us, 2.9 TB/s; 1 x 6144 x 6144 6.5 us
+//   16 tokens, top-8 of 80 experts, 4096 x 6144: 146 us, 93 % of the copy rate
+// What brought it there, at 8192 x 4096 x 6144: one CTA a tile, the accumulator
+// held while it was stored, 125 us; CTA pairs 111; outputs packed before the
+// hand-over by straight-line code that fits the instruction cache 74 (the
+// epilogue took longer than the K loop); at 256 x 6144 x 6144, all ranks' sums
+// loaded before the first is added and splits that fit the GPU at once, 48 us
+// to 13.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -1129,8 +1146,8 @@ static nvfp4_status check_product(const char* name, int M, const uint8_t* b_code
                                   const float* row_weight, const float* bias, int out_dtype, const void* y,
                                   long long y_stride) {
   NV_REQUIRE(M >= 0 && N >= 1 && K >= 1, NVFP4_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", name, M, N, K);
-  NV_REQUIRE(K <= (1 << 30) && N <= (1 << 30), NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: N=%d or K=%d is above 2^30", name, N,
-             K);
+  NV_REQUIRE(M <= (1 << 30) && N <= (1 << 30) && K <= (1 << 30), NVFP4_ERR_UNSUPPORTED_SHAPE,
+             "%s: M=%d, N=%d or K=%d is above 2^30", name, M, N, K);
   NV_REQUIRE(E >= 0 && E <= kXMaxE, NVFP4_ERR_UNSUPPORTED_SHAPE, "%s: E=%d is not in [0, %d]", name, E, kXMaxE);
   NV_REQUIRE((E > 0) == (offsets != nullptr) && (E > 0 || !counts), NVFP4_ERR_INVALID_ARG,
              "%s: expert_offsets (and expert_counts) go with E >= 1, E=%d", name, E);
@@ -1235,7 +1252,7 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long lo
 }
 
 extern "C" int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages) {
-  if (M < 1 || N < 1 || K < 1 || E < 0) return -1;
+  if (M < 1 || N < 1 || K < 1 || E < 0 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30) || E > kXMaxE) return -1;
   const MxPlan pl = plan_mx_gemm(M, N, K, E, 148);
   if (splits) *splits = pl.splits;
   if (pair) *pair = pl.pair ? 1 : 0;

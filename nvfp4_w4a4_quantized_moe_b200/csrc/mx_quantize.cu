@@ -477,8 +477,10 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const uint8_t
   }
 }
 
-// Units per group of lanes: several where that still leaves every SM a few
-// blocks, else one, so that a few rows spread over the whole GPU.
+// Units per group of lanes: two where that still leaves every SM eight blocks,
+// else one, so that a few rows spread over the whole GPU.  Measured, one
+// against two, 6144 columns of bf16 (us): 256 rows 1.75 and 1.83, 1600 rows
+// 4.9 and 4.7, 8192 rows 21.8 and 21.0, 65536 rows 170 and 157.
 constexpr int kMxUnits = 2;
 template <typename T>
 static inline bool many_units(uint32_t units, int sms) {

@@ -133,6 +133,20 @@ def test_quantize_gathers_rows():
     assert empty.rows == 0
 
 
+def test_canonical_scales_become_tiled_by_quantising_again():
+    require_cuda()
+    c = capi()
+    rng = np.random.default_rng(4)
+    rows, cols = 300, 1000
+    codes = rng.integers(0, 256, (rows, 512), dtype=np.uint8)
+    scales = rng.integers(0, 253, (rows, 32), dtype=np.uint8)
+    q = c.Mxfp4(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), rows, cols, "canonical")
+    for dt in (torch.float32, torch.bfloat16):
+        v = c.mxfp4_dequantize(q, dtype=dt)
+        t = c.mxfp4_quantize(v)
+        assert t.layout == "tiled" and torch.equal(c.mxfp4_dequantize(t, dtype=dt), v)
+
+
 def test_zero_rows_and_stacks():
     require_cuda()
     c = capi()

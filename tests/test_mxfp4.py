@@ -43,6 +43,20 @@ def test_mxfp4_scale_and_values():
     assert np.array_equal(mxfp4.dequantize(*mxfp4.quantize(v[ok]), 40), v[ok])
 
 
+def test_quantising_values_again_keeps_them():
+    """Any codes under any scale up to 2^125 (what 6 times it leaves finite):
+    the block's new scale may be smaller, the values stay."""
+    rng = np.random.default_rng(2)
+    codes = rng.integers(0, 256, (2000, 32), dtype=np.uint8)
+    codes[:500] &= 0x33                                    # blocks of small elements
+    codes[500:600] &= 0x11
+    codes[600:700] = 0
+    scales = rng.integers(0, 253, (2000, 2), dtype=np.uint8)
+    scales[:50] = 0
+    v = mxfp4.dequantize(codes, scales, 64)
+    assert np.array_equal(mxfp4.dequantize(*mxfp4.quantize(v), 64), v)
+
+
 def test_mxfp4_error_is_within_half_a_step():
     x = np.random.default_rng(0).standard_normal((50, 320)) * 3
     codes, scales = mxfp4.quantize(x)
@@ -131,7 +145,7 @@ def test_product_refusals():
     assert mm(E=2, off=FAKE, N=130, st=130) == 2 and mm(E=1025, off=FAKE) == 2
     assert mm(a=ctypes.c_void_p(0x1008)) == 1 and mm(y=ctypes.c_void_p(0x1001)) == 1
     assert mm(n=255) == 5 and mm(ws=None) == 5 and mm(ws=ctypes.c_void_p(0x1010)) == 5
-    assert mm(K=(1 << 30) + 1) == 2
+    assert mm(K=(1 << 30) + 1) == 2 and mm(M=(1 << 30) + 1, N=1, st=1) == 2 and mm(M=1 << 30, N=1 << 20, st=1 << 20) == 2
     assert mm(M=0) == 0
 
     def lin(x=FAKE, dt=0, r=4, st=64, perm=None, n=0, N=128, K=64, ws=FAKE, wsn=1 << 20):
@@ -180,8 +194,9 @@ def test_product_plans():
         assert plan(M, N, K)[2]
     assert plan(5632, 2048, 1312, 4)[2] and plan(6144, 1920, 1440, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
     assert plan(256, 256, 256)[0] == 128 and plan(1024, 4096, 6144)[0] == 256
-    with pytest.raises(ValueError):
-        plan(0, 1, 1)
+    for bad in ((0, 1, 1), ((1 << 30) + 1, 1, 1), (1, 1, 1, 1025)):
+        with pytest.raises(ValueError):
+            plan(*bad)
 
 
 def test_balance_refusals():
