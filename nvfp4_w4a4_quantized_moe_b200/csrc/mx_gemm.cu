@@ -14,7 +14,7 @@
 // empty, and a warp's 32 lanes hold 32 neighbouring outputs of one token, so
 // y leaves in whole sectors straight from registers for any N.
 //
-// One CTA per tile of 128 b rows x up to 256 tokens; warp 0 issues the loads
+// One CTA per tile of 128 b rows x up to 128 tokens; warp 0 issues the loads
 // (TMA for codes, bulk copies for scale atoms), warp 1 the MMAs, warps 2..9
 // drain the accumulator.  A K stage is 256 elements: 128-byte code rows in the
 // 128-byte swizzle, two scale atoms per 128 rows.
@@ -50,6 +50,7 @@
 namespace nvfp4moe {
 
 constexpr int kXBM = 128;                        // b rows per tile
+constexpr int kXNT = 128;                        // tokens per tile, at most
 constexpr int kXBK = 256;                        // K elements per stage
 constexpr int kXRowBytes = kXBK / 2;             // 128 bytes of codes per row and stage
 constexpr int kXWBytes = kXBM * kXRowBytes;      // 16 KiB
@@ -72,6 +73,7 @@ struct MxGemmParams {
   int n_wt, n_tt;            // b tiles (per expert), token tiles (dense)
   int nt;                    // tokens per tile
   int stages;
+  int n_acc;                 // accumulators that tiles alternate between
   int splits;                // K splits (CTAs per cluster)
   int pairs;                 // 16-bit y whose rows are 4-byte aligned (pair kernel)
   int quads;                 // y whose rows are aligned to four elements
@@ -87,12 +89,8 @@ struct MxGemmParams {
   uint32_t* status;
 };
 
-// One stage: b codes, token codes, b scales, token scales (1 KiB per started
-// 128 tokens).
-__host__ __device__ constexpr int mx_sf_tiles(int nt) { return (nt + 127) / 128; }
-__host__ __device__ constexpr int mx_stage_bytes(int nt) {
-  return kXWBytes + (nt * kXRowBytes + 1023) / 1024 * 1024 + kXSfBytes * (1 + mx_sf_tiles(nt));
-}
+// One stage: b codes, token codes, b scales, token scales.
+__host__ __device__ constexpr int mx_stage_bytes(int nt) { return kXWBytes + nt * kXRowBytes + 2 * kXSfBytes; }
 
 // Instruction descriptor: kind::mxf4, E2M1 x E2M1, UE8M0 scales, K-major
 // operands, M x N tile, the scales of byte pair `id` (0 or 2) of each word.
@@ -262,14 +260,16 @@ __global__ void __launch_bounds__(kXThreads, 2)
   __shared__ int abort_s;
   volatile int* abort_flag = &abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Tiles of up to 128 tokens alternate between two accumulators, so that the
-  // next tile's MMAs run while one is drained; 256 columns leave room for one.
+  // A CTA that has its SM to itself alternates between two accumulators, so
+  // that the next tile's MMAs run while one is drained; of two CTAs on an SM
+  // one works while the other drains, and wide ones have half of tensor memory
+  // each, room for one.
   const int nt_pad = max(p.nt, 32);                          // columns of an accumulator
-  const int n_acc = p.nt <= 128 ? 2 : 1;
-  const uint32_t need = (uint32_t)(n_acc * nt_pad) + 4 * kXAtoms * (1 + 2);
+  const int n_acc = p.n_acc;
+  const uint32_t need = (uint32_t)(n_acc * nt_pad) + 4 * kXAtoms * 2;
   const uint32_t tcols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
   const int stage_bytes = mx_stage_bytes(p.nt);
-  const int x_bytes = (p.nt * kXRowBytes + 1023) / 1024 * 1024;
+  const int x_bytes = p.nt * kXRowBytes;                     // nt is a multiple of 16: whole 8-row swizzle groups
   // this CTA's share of K
   const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
   const int kt0 = (int)((long long)p.kt_total * rank / p.splits);
@@ -349,7 +349,6 @@ __global__ void __launch_bounds__(kXThreads, 2)
       const bool whole = p.E == 0 || c.tokens > p.nt - 32;
       const int boxes = (c.tokens + 31) / 32;
       const uint32_t xb = (uint32_t)(whole ? p.nt : boxes * 32) * kXRowBytes;
-      const int sft = mx_sf_tiles(c.tokens);
       for (int i = 0; i < nkt; ++i, ++issued) {
         ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag));
         if (!ok) {
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kXThreads, 2)
           uint8_t* sX = smem + stage * stage_bytes + kXWBytes;
           uint8_t* sSFX = sX + x_bytes + kXSfBytes;
           const uint32_t sf_bytes = (uint32_t)min(kXAtoms, p.groups - kt * kXAtoms) * kAtomBytes;
-          mbar_arrive_expect_tx(&full_bar[stage], kXWBytes + xb + sf_bytes * (uint32_t)(1 + sft));
+          mbar_arrive_expect_tx(&full_bar[stage], kXWBytes + xb + 2 * sf_bytes);
           if (issued >= early) load_b(c.wt, c.e, kt, stage);
           if (whole) {
             tma_load_2d(sX, &tmX, kt * kXRowBytes, c.row0, &full_bar[stage]);
@@ -372,9 +371,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
             for (int b = 0; b < boxes; ++b)
               tma_load_2d(sX + b * 32 * kXRowBytes, &tmX32, kt * kXRowBytes, c.row0 + 32 * b, &full_bar[stage]);
           }
-          for (int h = 0; h < sft; ++h)
-            bulk_load(sSFX + h * kXSfBytes, p.a_sf + (size_t)(c.row0 / kRowTile + h) * sf_tile + (size_t)kt * kXSfBytes,
-                      sf_bytes, &full_bar[stage]);
+          bulk_load(sSFX, p.a_sf + (size_t)(c.row0 / kRowTile) * sf_tile + (size_t)kt * kXSfBytes, sf_bytes,
+                    &full_bar[stage]);
         }
         __syncwarp();
         filled |= 1u << stage;
@@ -402,7 +400,7 @@ __global__ void __launch_bounds__(kXThreads, 2)
     const uint64_t sfw0 = sdesc_scale_atom(s0 + kXWBytes + x_bytes);
     const uint64_t sfx0 = sdesc_scale_atom(s0 + kXWBytes + x_bytes + kXSfBytes);
     const uint64_t stage_step = (uint64_t)stage_bytes >> 4;
-    constexpr uint64_t kAtomStep = kAtomBytes >> 4, kSfStep = kXSfBytes >> 4;
+    constexpr uint64_t kAtomStep = kAtomBytes >> 4;
     const uint32_t sfw_t = tmem + (uint32_t)(n_acc * nt_pad), sfx_t = sfw_t + 4 * kXAtoms;
     int stage = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
@@ -410,7 +408,6 @@ __global__ void __launch_bounds__(kXThreads, 2)
     for (int t = t_first; ok && t < num_tiles; t += t_step) {
       const MxTile c = mx_tile(p, segs, t);
       const int n_mma = (c.tokens + 15) & ~15;
-      const bool two = c.tokens > kRowTile;
       const uint32_t id0 = idesc_mxf4(kXBM, n_mma, 0), id2 = idesc_mxf4(kXBM, n_mma, 2);
       ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty_bar[buf], acc_phase ^ 1u, abort_flag));
       if (!ok) {
@@ -435,26 +432,22 @@ __global__ void __launch_bounds__(kXThreads, 2)
         const bool whole = p.groups - (kt0 + i) * kXAtoms >= kXAtoms;     // else K ends with one atom
         if (elected) {
           const uint64_t d = (uint64_t)stage * stage_step;
-          // straight-line code for each of the four shapes of a stage: a
-          // branch per instruction would starve the tensor pipe
-          auto issue = [&](auto n_atoms, auto both) {
+          // straight-line code for either length of a stage: a branch per
+          // instruction would starve the tensor pipe
+          auto issue = [&](auto n_atoms) {
             constexpr int A = decltype(n_atoms)::value;
 #pragma unroll
             for (int j = 0; j < A; ++j) {
               tc_cp_scale_atom(sfw_t + 4 * j, sfw0 + d + j * kAtomStep);
-              tc_cp_scale_atom(sfx_t + 8 * j, sfx0 + d + j * kAtomStep);
-              if constexpr (decltype(both)::value)
-                tc_cp_scale_atom(sfx_t + 8 * j + 4, sfx0 + d + kSfStep + j * kAtomStep);
+              tc_cp_scale_atom(sfx_t + 4 * j, sfx0 + d + j * kAtomStep);
             }
 #pragma unroll
             for (int j = 0; j < 2 * A; ++j)          // 64 elements = 32 bytes of K per MMA, two per atom
               mma_mxf4(acc_t, w0 + d + 2 * j, x0 + d + 2 * j, (j & 1) ? id2 : id0, sfw_t + 4 * (j >> 1),
-                       sfx_t + 8 * (j >> 1), accumulate | j);
+                       sfx_t + 4 * (j >> 1), accumulate | j);
           };
-          if (whole && two) issue(std::integral_constant<int, kXAtoms>{}, std::true_type{});
-          else if (whole) issue(std::integral_constant<int, kXAtoms>{}, std::false_type{});
-          else if (two) issue(std::integral_constant<int, 1>{}, std::true_type{});
-          else issue(std::integral_constant<int, 1>{}, std::false_type{});
+          if (whole) issue(std::integral_constant<int, kXAtoms>{});
+          else issue(std::integral_constant<int, 1>{});
           tc_commit(&empty_bar[stage]);
         }
         __syncwarp();
@@ -931,26 +924,22 @@ struct MxGemmArgs {
 
 // Tile width, pipeline depth and K splits of a product (host arithmetic).
 struct MxPlan {
-  int nt, stages, splits, ctas_per_sm;
+  int nt, stages, splits, ctas_per_sm, n_acc;
   bool pair;
 };
 
-// Tiles of 128 or 256 tokens on one CTA, or of 384 on a pair: the one whose
-// waves are estimated to end first, fitted to measurements of one to seven
-// waves (one B200; us for each K stage and hand-over of a wave, and once for
-// start and end).  Measured, waves: us
-//   K = 6144 (24 stages)   128 tokens  1: 12.5  2: 20.7  3: 29.4  4: 37.4  7: 61.8
-//                          256 tokens  1: 15.7  2: 28.4  4: 53.5
-//                          pair        1: 18.7  2: 29.6  3: 41.5
-//   K = 1024 (4 stages)    128 tokens  1: 6.7   2: 8.3   4: 13.0
-//                          256 tokens  1: 8.2   2: 13.0
-//                          pair        1: 9.4   2: 14.0
-struct MxWave {
-  int nt;
-  double stage, wave, once;
-};
-constexpr MxWave kMxWaves[3] = {{128, 0.30, 0.9, 4.5}, {256, 0.385, 3.2, 3.2}, {kPNT, 0.32, 3.3, 6.5}};
-
+// Tiles of up to 128 tokens on one CTA, or of 384 on a pair: the kind whose
+// waves are estimated to end first, fitted to measurements (one B200, us).
+// One CTA has its SM to itself while that gives every tile an SM, else two
+// share one.  Measured, waves (of 148 tiles, 296 shared, 74 pairs): us
+//   K = 6144 (24 stages)   alone   1: 12.5  2: 20.7  3: 29.4
+//                          shared  1: 15.8  2: 26.3  (128 tiles: 14.1)
+//                          pairs   1: 18.7  2: 29.6  3: 41.5
+//   K = 1024 (4 stages)    alone   1: 5.8   2: 8.4
+//                          shared  1: 7.3
+//                          pairs   1: 9.4   2: 14.0
+// and 16 experts of 32 tokens, 6144 x 2048 (768 tiles): alone 25.3, shared
+// 22.4.  (256 tokens a tile, one wave of 148 at K = 6144, took 15.1 to 16.1.)
 static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   const int kt = (mx_groups(K) + kXAtoms - 1) / kXAtoms;
   const int n_wt = (N + kXBM - 1) / kXBM;
@@ -958,43 +947,39 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   // tokens an expert, taken as even; grouped rows hold up to 127 of padding an
   // expert (moe_route's capacity has that many)
   const long long per = E == 0 ? M : std::max(16ll, (long long)M / E - 127);
+  const long long tiles = (long long)n_wt * experts * ((per + kXNT - 1) / kXNT);
+  const bool shared = tiles > sms;
+  const double us = shared ? 4.6 + (double)((tiles + 2 * sms - 1) / (2 * sms)) * (0.43 * kt + 0.9) : 5.4 + 0.30 * kt;
+  const long long pairs = (long long)((n_wt + 1) / 2) * experts * ((per + kPNT - 1) / kPNT);
+  const double pair_us = 6.5 + (double)((pairs + sms / 2 - 1) / (sms / 2)) * (0.32 * kt + 3.3);
   MxPlan pl;
-  pl.splits = pl.ctas_per_sm = 1;
-  int best = 0;
-  double best_us = 0;
-  for (int i = 0; i < (E <= kPMaxE ? 3 : 2); ++i) {
-    const MxWave& w = kMxWaves[i];
-    const bool pair = i == 2;
-    const long long tiles = (long long)(pair ? (n_wt + 1) / 2 : n_wt) * experts * ((per + w.nt - 1) / w.nt);
-    const long long slots = pair ? sms / 2 : sms;
-    const double us = w.once + (double)((tiles + slots - 1) / slots) * (w.stage * kt + w.wave);
-    if (i == 0 || us < best_us) {
-      best = i;
-      best_us = us;
-    }
-  }
-  pl.pair = best == 2;
-  pl.nt = kMxWaves[best].nt;
+  pl.splits = pl.ctas_per_sm = pl.n_acc = 1;
+  pl.pair = pair_us < us && E <= kPMaxE;
   if (pl.pair) {
+    pl.nt = kPNT;
     pl.stages = kPStages;
     return pl;
   }
   // a single token tile is no wider than its tokens
-  if (E == 0 && M <= pl.nt) pl.nt = (M + 15) / 16 * 16;
+  pl.nt = E == 0 && M <= kXNT ? (M + 15) / 16 * 16 : kXNT;
   // Few tokens: two CTAs on an SM, and K split over a cluster while there are
   // SMs for it.  Measured at N = K = 6144 (48 tiles) and one token, splits of
   // 1, 2, 3, 4, 6, 8: 10.8, 7.8, 7.6, 7.0, 11.4, 11.2 us; at N = 1024 (8
   // tiles) 10.2, 6.9, 5.8, 5.1, 4.7, 4.4; at N = 5001, K = 2010 (40 tiles) 6.0,
   // 5.7, 5.5, 6.6, 6.7, 11.0; wider tiles, at one CTA an SM (128 tokens, 48
   // tiles): 12.2, 11.2, then 17 and more, as clusters of three and more no
-  // longer fit at once.
-  pl.ctas_per_sm = pl.nt <= 64 ? 2 : 1;
-  const int room = (pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - mx_segment_bytes(E);
-  pl.stages = std::min(kXMaxStages, room / mx_stage_bytes(pl.nt));
+  // longer fit at once; with 16 tiles (100 x 2048 x 6144) 11.6, 9.3, 7.8, 7.2,
+  // 7.5, 13.4.  Joining 128 columns costs 2 us: at 8 stages (128 x 4096 x 2048)
+  // one split takes 6.8 us, two 7.4, at 16 (128 x 6144 x 4096) 9.5 and 9.1.
+  const int table = mx_segment_bytes(E), stage = mx_stage_bytes(pl.nt);
+  // (a table of very many experts leaves two CTAs too few stages each)
+  pl.ctas_per_sm = (pl.nt <= 64 || shared) && (kXSmemPair - 1024 - table) / stage >= 3 ? 2 : 1;
+  pl.n_acc = pl.nt <= 64 || pl.ctas_per_sm == 1 ? 2 : 1;
+  pl.stages = std::min(kXMaxStages, ((pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - table) / stage);
   if (E == 0) {
-    const long long tiles = (long long)n_wt * ((M + pl.nt - 1) / pl.nt);
-    const long long most = pl.ctas_per_sm == 2 || tiles * 4 <= sms / 2 ? 4 : 2;
-    pl.splits = (int)std::max(1ll, std::min({most, sms / tiles, (long long)(kt + 1) / 2}));
+    const long long all = (long long)n_wt * ((M + pl.nt - 1) / pl.nt);
+    const long long most = pl.nt <= 64 ? 4 : kt < 12 ? 1 : all * 4 <= sms / 2 ? 4 : 2;
+    pl.splits = (int)std::max(1ll, std::min({most, sms / all, (long long)(kt + 1) / 2}));
   }
   return pl;
 }
@@ -1092,6 +1077,7 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   p.nt = pl.nt;
   p.n_tt = a.E ? 0 : (a.M + pl.nt - 1) / pl.nt;
   p.stages = pl.stages;
+  p.n_acc = pl.n_acc;
   p.splits = pl.splits;
   p.early_b = a.early_b;
   const int elem = mx_elem_size(a.out_dtype), access = row_access_bytes(a.y, a.M > 1 ? a.y_stride * elem : 0, elem);

@@ -193,11 +193,13 @@ def product_bound(a, b, ref, dtype, row_weight=None, bias=None):
 
 
 MNK = [(3, 5, 1), (1, 1, 32), (1, 128, 64), (1, 6144, 512), (2, 7, 33), (15, 130, 96), (16, 256, 128), (17, 500, 160),
-       (31, 64, 256), (32, 129, 288), (33, 1000, 544), (64, 384, 1024), (65, 128, 100), (100, 300, 2048),
+       (31, 64, 256), (32, 129, 288), (33, 1000, 544), (64, 384, 1024), (65, 128, 100), (100, 300, 2048), (100, 300, 5000), (128, 6000, 4500),
        (128, 128, 512), (129, 255, 320), (200, 1024, 640), (256, 256, 256), (257, 130, 224), (300, 700, 384),
        (515, 129, 1056), (1024, 1536, 256), (3000, 257, 96), (16, 128, 6144), (5, 260, 4000),
        # on CTA pairs (tests/test_mxfp4.py checks that these sizes reach them), K ending with one atom and two
-       (1536, 4096, 1312), (1500, 3999, 1400), (3000, 2049, 1700)]
+       (2990, 2290, 1900), (3000, 2049, 1700),
+       # two CTAs on an SM, and their second wave
+       (3000, 1000, 96), (2990, 2290, 300)]
 
 
 @pytest.mark.parametrize("M,N,K", MNK)
@@ -235,7 +237,7 @@ def test_matmul_bias_row_weight_and_strided_out():
     require_cuda()
     c = capi()
     rng = np.random.default_rng(5)
-    for M, N, K in [(3, 200, 320), (3, 200, 2048), (40, 130, 96), (300, 300, 256), (1500, 3999, 1400)]:
+    for M, N, K in [(3, 200, 320), (3, 200, 2048), (40, 130, 96), (300, 300, 256), (2990, 2290, 1900), (3000, 2049, 1700)]:
         a, av = operand(M, K, 1)
         b, bv = operand(N, K, 2)
         bias = rng.standard_normal(N).astype(np.float32)
@@ -249,11 +251,11 @@ def test_matmul_bias_row_weight_and_strided_out():
         assert (big[:, :5] == 7.0).all() and (big[:, 5 + N:] == 7.0).all()
 
 
-@pytest.mark.parametrize("M", [1, 40, 300, 1500])
+@pytest.mark.parametrize("M", [1, 40, 300, 2990])
 def test_a_nan_block_reaches_its_row_only(M):
     require_cuda()
     c = capi()
-    N, K = (200, 300) if M < 1500 else (3999, 1420)
+    N, K = (200, 300) if M < 2990 else (2290, 1900)
     a, av = operand(M, K, 3)
     b, bv = operand(N, K, 4)
     clean = c.mxfp4_matmul(a, b)
@@ -271,7 +273,7 @@ def test_padding_bytes_do_not_matter():
     """Scale bytes of padding rows may hold anything, NaN included."""
     require_cuda()
     c = capi()
-    for M, N, K in [(3, 70, 100), (150, 260, 300), (1500, 3999, 1400)]:
+    for M, N, K in [(3, 70, 100), (150, 260, 300), (2990, 2290, 1900)]:
         a, av = operand(M, K, 8)
         b, bv = operand(N, K, 9)
         want = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
@@ -298,8 +300,8 @@ def grouped_case(counts, gaps, N, K, seed):
     ([3] * 40, [0] * 40, 128, 512),
     ([1000, 0, 257], [0, 0, 0], 384, 160),
     ([0, 0, 0], [0, 1, 0], 128, 96),
-    ([1500, 0, 385, 3500], [0, 0, 0, 0], 2048, 1312),        # on CTA pairs
-    ([1500, 1536, 1, 2900], [0, 0, 0, 0], 1920, 1440),        # pairs, an odd number of 128-row b tiles per expert
+    ([900, 0, 385, 1900], [0, 0, 0, 0], 2048, 1700),        # on CTA pairs
+    ([1000, 1024, 1, 1200], [0, 0, 0, 0], 1920, 1900),        # pairs, an odd number of 128-row b tiles per expert
 ])
 def test_grouped_matmul(counts, gaps, N, K):
     require_cuda()
@@ -386,7 +388,7 @@ def test_grouped_linear_with_padding_rows(with_counts):
 def test_results_do_not_change_from_run_to_run():
     require_cuda()
     c = capi()
-    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024), (1536, 4096, 1312)]:
+    for M, N, K in [(1, 1000, 4096), (48, 512, 2048), (600, 640, 1024), (2990, 2290, 1900)]:
         a, _ = operand(M, K, 1)
         b, _ = operand(N, K, 2)
         first = c.mxfp4_matmul(a, b, out_dtype=torch.float32)
@@ -437,8 +439,8 @@ import sys, torch
 sys.path.insert(0, %r)
 from nvfp4_w4a4_quantized_moe_b200 import capi as c
 torch.manual_seed(0)
-x = [torch.randn(m, 640, device="cuda").bfloat16() for m in (1, 300, 1536)]
-w = torch.randn(4096, 640, device="cuda").bfloat16()
+x = [torch.randn(m, 1900, device="cuda").bfloat16() for m in (1, 300, 2990)]
+w = torch.randn(2290, 1900, device="cuda").bfloat16()
 l = torch.randn(3000, 64, device="cuda")
 idx = l.topk(4).indices.int()
 one = torch.ones(1, device="cuda")

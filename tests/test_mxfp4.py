@@ -171,29 +171,26 @@ def test_product_plans():
                 kt = -(-K // 256)
                 assert 1 <= splits <= 8 and splits <= kt
                 assert nt % 16 == 0 and (nt == 384) == pair
-                assert nt >= min(M, 128) and (nt % 128 == 0 or nt >= M)    # a narrow tile is the only one
-                assert stages >= 3
+                assert nt >= min(M, 128) and stages >= 3
                 if not pair:
-                    # two accumulators up to 128 columns, then the scales: within tensor memory
-                    acc = max(nt, 32) * (2 if nt <= 128 else 1)
-                    assert acc + 24 <= 512 and nt <= 256
+                    assert nt <= 128
                     # the split's partial sums fit the stages they overlay
-                    stage = 16384 + nt * 128 + 1024 * (1 + -(-nt // 128))
+                    stage = 16384 + nt * 128 + 2048
                     assert splits == 1 or nt * 512 <= stages * stage
-                    assert stages * stage + 1024 <= (227 * 1024 - 256 if nt > 64 else 114 * 1024 - 1024 - 256)
+                    assert stages * stage + 1024 <= 227 * 1024 - 256
             for E in (1, 8, 80, 481, 1024):
                 if N % 128 == 0 and M % 128 == 0:
                     nt, splits, pair, stages = plan(M, N, 2048, E)
-                    assert nt in (128, 256, 384) and splits == 1 and not (pair and E > 480)
-                    stage = 16384 + nt * 128 + 1024 * (1 + nt // 128)
+                    assert nt in (128, 384) and splits == 1 and not (pair and E > 480) and stages >= 3
                     if not pair:
-                        assert stages * stage + (3 * E + 1) * 4 + 1024 <= 227 * 1024 - 256
-    assert plan(1, 6144, 512)[1] == 1 and plan(16, 128, 6144)[1] == 4 and plan(100, 300, 2048)[1] == 4
+                        assert stages * 34816 + (3 * E + 1) * 4 + 1024 <= 227 * 1024 - 256
+    assert plan(1, 6144, 512)[1] == 1 and plan(16, 128, 6144)[1] == 4 and plan(100, 300, 2048)[1] == 1 and plan(100, 300, 6144)[1] == 4
     assert plan(1, 1000, 4096) == (16, 4, False, 5)
-    for M, N, K in ((1536, 4096, 1312), (1500, 3999, 1400), (1500, 3999, 1420), (3000, 2049, 1700)):
+    for M, N, K in ((2990, 2290, 1900), (3000, 2049, 1700)):
         assert plan(M, N, K)[2]
-    assert plan(5632, 2048, 1312, 4)[2] and plan(6144, 1920, 1440, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
-    assert plan(256, 256, 256)[0] == 128 and plan(1024, 4096, 6144)[0] == 256
+    assert plan(3456, 2048, 1700, 4)[2] and plan(3456, 1920, 1900, 4)[2] and plan(1152, 512, 96, 3)[0] == 128
+    # alone on an SM (six stages), and two on an SM (three)
+    assert plan(256, 256, 256) == (128, 1, False, 6) and plan(3000, 1000, 96) == (128, 1, False, 3)
     for bad in ((0, 1, 1), ((1 << 30) + 1, 1, 1), (1, 1, 1, 1025)):
         with pytest.raises(ValueError):
             plan(*bad)
