@@ -622,8 +622,8 @@ def moe_nvfp4_down(W: MoeWeights, h_codes, h_scales, expert_offsets, expert_coun
 #: Element types of unquantised matrices (MXFP4_DTYPE_*).
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-# A small call is bound by its host side (17 us for mxfp4_linear of one token,
-# of which the GPU works 10), so the functions below read each property of a
+# A small call is bound by its host side (16 us for mxfp4_linear of one token,
+# of which the GPU works 8), so the functions below read each property of a
 # tensor once, take the current stream as the raw handle and give
 # torch.empty its sizes one by one (a tuple costs 0.7 us more).
 _raw_stream = torch._C._cuda_getCurrentRawStream

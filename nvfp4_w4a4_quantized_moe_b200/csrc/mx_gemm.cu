@@ -33,13 +33,14 @@
 //                        bf16 rate)
 //   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 8.6
 //   16 x 6144 x 6144     6.8 us, 2.9 TB/s; 1 x 6144 x 6144 6.5 us
-//   16 tokens, top-8 of 80 experts, 4096 x 6144: 146 us, 93 % of the copy rate
+//   16 tokens, top-8 of 80 experts, 4096 x 6144: 140 us, 97 % of the copy rate
 // What brought it there, at 8192 x 4096 x 6144: one CTA a tile, the accumulator
 // held while it was stored, 125 us; CTA pairs 111; outputs packed before the
 // hand-over by straight-line code that fits the instruction cache 74 (the
 // epilogue took longer than the K loop); at 256 x 6144 x 6144, all ranks' sums
 // loaded before the first is added and splits that fit the GPU at once, 48 us
-// to 13.
+// to 13; two CTAs on an SM where there are more tiles than SMs, the 80 experts
+// 146 us to 140.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
