@@ -12,7 +12,7 @@
 // of b, its N columns are rows of a ("tokens").  A decoding step's few tokens
 // are then a narrow N (16 columns) instead of a 128-row tile that is nearly
 // empty, and a warp's 32 lanes hold 32 neighbouring outputs of one token, so
-// y leaves in whole sectors straight from registers for any N.
+// y leaves straight from registers, coalesced for any N.
 //
 // One CTA per tile of 128 b rows x up to 128 tokens; warp 0 issues the loads
 // (TMA for codes, bulk copies for scale atoms), warp 1 the MMAs, warps 2..9
