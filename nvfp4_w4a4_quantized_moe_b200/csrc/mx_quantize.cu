@@ -42,8 +42,9 @@ template <typename T> __host__ __device__ constexpr int block_subs() { return kM
 //   read  16384 x 6146 bf16 (4 B)       61             72           59
 //   read  8192 x 6145 fp32 (4 B)        58             58           50
 //   read  8191 x 6100 fp16 (8 B)        23             31           35
-//   write 16384 x 6145 bf16 (2 B)      544             68
-//   write 8191 x 6100 fp16 (8 B)        53             27
+//   write 16384 x 6145 bf16 (2 B)      544             71
+//   write 16384 x 6146 bf16 (4 B)        -             52
+//   write 8191 x 6100 fp16 (8 B)        53             25
 constexpr bool is_narrow(int vb) { return vb < 16; }
 constexpr int kMxWarpBytes = 1024;
 
@@ -63,6 +64,21 @@ NVDEV void store_staged(uint8_t* out, int cols, long long stride_bytes, int row,
   mine[0] = make_uint4(w[0], w[1], w[2], w[3]);
   mine[1] = make_uint4(w[4], w[5], w[6], w[7]);
   __syncwarp();
+  if constexpr (VB >= 4) {
+    // the usual case, every unit whole: no checks
+    if (__all_sync(0xffffffffu, real && grp * kMxGroup + kMxGroup <= cols)) {
+      using V = typename Narrow<VB>::type;
+      uint8_t* own = out + (size_t)row * (size_t)stride_bytes + (size_t)grp * unit_bytes;
+#pragma unroll
+      for (int unit = 0; unit < 32 / LPU; ++unit) {
+        V* to = reinterpret_cast<V*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(own), unit * LPU)) + lane;
+        const V* from = reinterpret_cast<const V*>(buf + unit * unit_bytes) + lane;
+#pragma unroll
+        for (int it = 0; it < unit_bytes / (32 * VB); ++it) to[it * 32] = from[it * 32];
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int unit = 0; unit < 32 / LPU; ++unit) {
     const int r = __shfl_sync(0xffffffffu, row, unit * LPU), g = __shfl_sync(0xffffffffu, grp, unit * LPU);
@@ -448,8 +464,13 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const uint8_t
     float v[EPL];
 #pragma unroll
     for (int h = 0; h < EPL / 8; ++h) mx_values8(q[i][h], v + 8 * h);
+    const uint64_t S2 = pack_f32x2(S, S);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] = __fmul_rn(v[j], S);
+    for (int j = 0; j < EPL; j += 2) {
+      const uint64_t r = mul_f32x2(pack_f32x2(v[j], v[j + 1]), S2);
+      v[j] = lo_f32(r);
+      v[j + 1] = hi_f32(r);
+    }
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
