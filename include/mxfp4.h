@@ -100,8 +100,9 @@ NVFP4_API nvfp4_status mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_sca
 
 /* The product with a = x (or x[perm]) quantised in the call: mxfp4_quantize
  * into the workspace, then mxfp4_matmul on its M rows (M = perm_rows with
- * perm, else rows).  The workspace's status word is that of the product.  y
- * may take the place of x. */
+ * perm, else rows).  A dense product of few rows quantises them itself, with
+ * the same result.  The workspace's status word is that of the product.  y may
+ * take the place of x. */
 NVFP4_API size_t mxfp4_linear_workspace_size(int M, int K);
 NVFP4_API nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long long row_stride, const int32_t* perm,
                                     int perm_rows, const uint8_t* b_codes, const uint8_t* b_scales, int N, int K,

@@ -101,6 +101,13 @@ NVFP4_API int nvfp4_test_router_splits(int T, int H, int* stages_per_split);
  * for sizes that mxfp4_matmul refuses. */
 NVFP4_API int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages);
 
+/* Host arithmetic only: whether a dense mxfp4_linear of M rows of `dtype`
+ * quantises them inside the product (on 148 SMs, y apart from x); `wide`: the
+ * rows of x are 16-byte aligned.  Then *stages (nullable) gets the pipeline
+ * stages and *ctas_per_sm (nullable) the CTAs that an SM is to hold.  -1 for
+ * sizes that mxfp4_linear refuses. */
+NVFP4_API int nvfp4_test_mxfp4_fuses(int M, int N, int K, int dtype, int wide, int* stages, int* ctas_per_sm);
+
 #ifdef __cplusplus
 }
 #endif

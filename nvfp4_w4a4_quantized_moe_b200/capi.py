@@ -1,10 +1,10 @@
 """ctypes binding of libnvfp4moe.so (argument marshalling only).
 
 Every function here has the name of the C entry point it calls (see
-``include/nvfp4_moe.h``, ``include/mxfp4.h`` and ``include/moe_balance.h``) and does nothing but check tensor placement, dtypes
-and shapes, allocate outputs and workspace with torch, pass raw device
-pointers and torch's current CUDA stream, and turn a non-OK status into an
-exception.  All arithmetic of the layer runs in the library's CUDA kernels;
+``include/nvfp4_moe.h``, ``include/mxfp4.h`` and ``include/moe_balance.h``)
+and does nothing but check tensor placement, dtypes and shapes, allocate
+outputs and workspace with torch, pass raw device pointers and torch's current
+CUDA stream, and turn a non-OK status into an exception.  All arithmetic of the layer runs in the library's CUDA kernels;
 there is no CPU path.  Importing this module loads the library and fails
 loudly when it has not been built.
 """
@@ -125,6 +125,7 @@ _declare("nvfp4_test_block_scale_div", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp
 _declare("nvfp4_test_router_splits", _i, _i, _i, ctypes.POINTER(ctypes.c_int))
 _declare("nvfp4_test_mxfp4_plan", _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
          ctypes.POINTER(ctypes.c_int))
+_declare("nvfp4_test_mxfp4_fuses", _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int))
 
 # Every symbol the public headers declare (checked by the CPU test suite).
 EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
@@ -142,7 +143,7 @@ EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "nvfp4_test_e2m1", "nvfp4_test_e2m1_sweep", "nvfp4_test_e4m3", "nvfp4_test_sigmoid",
            "nvfp4_test_mma_peak", "nvfp4_test_wait_timeout", "nvfp4_test_block_scale_div",
-           "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan")
+           "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan", "nvfp4_test_mxfp4_fuses")
 
 
 def _check(status: int):
@@ -622,7 +623,7 @@ def moe_nvfp4_down(W: MoeWeights, h_codes, h_scales, expert_offsets, expert_coun
 #: Element types of unquantised matrices (MXFP4_DTYPE_*).
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-# A small call is bound by its host side (16 us for mxfp4_linear of one token,
+# A small call is bound by its host side (14 us for mxfp4_linear of one token,
 # of which the GPU works 8), so the functions below read each property of a
 # tensor once, take the current stream as the raw handle and give
 # torch.empty its sizes one by one (a tuple costs 0.7 us more).
@@ -1015,6 +1016,16 @@ def nvfp4_test_mxfp4_plan(M: int, N: int, K: int, E: int = 0):
     if nt < 0:
         raise ValueError(f"no MXFP4 product has M={M} N={N} K={K} E={E}")
     return nt, v[0].value, bool(v[1].value), v[2].value
+
+
+def nvfp4_test_mxfp4_fuses(M: int, N: int, K: int, dtype: torch.dtype, wide: bool = True):
+    """(pipeline stages, CTAs per SM) of a dense mxfp4_linear that quantises x
+    inside the product, None where a kernel before it does."""
+    v = [ctypes.c_int(0) for _ in range(2)]
+    r = lib.nvfp4_test_mxfp4_fuses(M, N, K, _DTYPES[dtype], int(wide), *(ctypes.byref(x) for x in v))
+    if r < 0:
+        raise ValueError(f"no MXFP4 product has M={M} N={N} K={K}")
+    return (v[0].value, v[1].value) if r else None
 
 
 def nvfp4_test_sigmoid(l: torch.Tensor):

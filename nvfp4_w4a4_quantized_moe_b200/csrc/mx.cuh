@@ -146,6 +146,103 @@ NVDEV void store_words8(void* p, const uint32_t* w) {
   }
 }
 
+// A lane's share of a 128-element unit is 32 bytes of the source, eight words:
+// 16 elements of a 16-bit type (8 lanes a unit, 2 a block) or 8 of fp32 (16
+// lanes, 4 a block).  One 256-bit access a lane where the rows allow it.
+template <typename T> __host__ __device__ constexpr int lane_elems() { return 32 / T::size; }
+template <typename T> __host__ __device__ constexpr int unit_lanes() { return kMxGroup / lane_elems<T>(); }
+
+// Elements at or past `n` read as 0.  `lo` and `hi` bound the matrix's bytes:
+// the aligned pieces of a narrow row may reach into its neighbours, not past
+// the matrix.
+template <typename T, int VB>
+NVDEV void load_share(const uint8_t* row, int c, int n, const uint8_t* lo, const uint8_t* hi, uint32_t* w) {
+  constexpr int EPL = lane_elems<T>();
+  if (c + EPL <= n) {
+    const uint8_t* at = row + (size_t)c * T::size;
+    if constexpr (VB >= 8) {
+      load_words8<VB>(at, w);
+      return;
+    } else {
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15u);
+      const uint8_t* base = at - off;
+      if (base >= lo && base + 48 <= hi) {
+        uint32_t r[12];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(base) + i);
+          r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+        }
+        // whole words by two conditional moves, the rest by funnel shifts
+#pragma unroll
+        for (int i = 0; i < 10; ++i) r[i] = (off & 8u) ? r[i + 2] : r[i];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) r[i] = (off & 4u) ? r[i + 1] : r[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = T::size == 4 ? r[i] : __funnelshift_r(r[i], r[i + 1], (off & 3u) * 8u);
+        return;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 0u;
+  if constexpr (T::size == 2) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (c + i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+  } else {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (c + i < n) w[i] = __ldg(p + i);
+  }
+}
+
+// mag_bits of the largest element of the block that these lanes share
+// (magnitudes compare as integers; packed pairs for 16-bit types).
+template <typename T>
+NVDEV uint32_t share_amax(const uint32_t* w) {
+  if constexpr (T::size == 2) {
+    uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return T::mag(max(m & 0xFFFFu, m >> 16));
+  } else {
+    uint32_t m = w[0] & 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
+}
+template <typename T>
+NVDEV float share_value(const uint32_t* w, int i) {
+  if constexpr (T::size == 2) return (i & 1) ? T::hi(w[i >> 1]) : T::lo(w[i >> 1]);
+  else return __uint_as_float(w[i]);
+}
+
+// A lane's share of a unit -> its codes, and the scale bytes of the lane's
+// block and (in the unit's first lane) the three behind it.  Whole warps.
+template <typename T>
+NVDEV void mx_unit(const uint32_t* w, uint32_t* q, uint32_t& sf) {
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>();
+  const uint32_t s = mx_scale(share_amax<T>(w));
+  const float inv = mx_inv_scale(s);
+#pragma unroll
+  for (int h = 0; h < EPL / 8; ++h) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = share_value<T>(w, h * 8 + j);
+    q[h] = mx_codes8(v, inv, s == 255u);
+  }
+  const uint32_t s1 = __shfl_down_sync(0xffffffffu, s, LPU / 4, LPU);
+  const uint32_t s2 = __shfl_down_sync(0xffffffffu, s, LPU / 2, LPU);
+  const uint32_t s3 = __shfl_down_sync(0xffffffffu, s, LPU / 4 * 3, LPU);
+  sf = s | (s1 << 8) | (s2 << 16) | (s3 << 24);
+}
+
 inline int mx_elem_size(int dtype) { return dtype == MXFP4_DTYPE_F32 ? 4 : 2; }
 inline bool mx_dtype_ok(int dtype) { return dtype >= MXFP4_DTYPE_BF16 && dtype <= MXFP4_DTYPE_F32; }
 

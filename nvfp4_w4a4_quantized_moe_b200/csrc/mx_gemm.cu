@@ -33,6 +33,7 @@
 //                        bf16 rate)
 //   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 8.6
 //   16 x 6144 x 6144     6.8 us, 2.9 TB/s; 1 x 6144 x 6144 6.5 us
+//   1 x 6144 x 6144 with x quantised in the same kernel 7.9 us (two kernels 9.5)
 //   16 tokens, top-8 of 80 experts, 4096 x 6144: 140 us, 97 % of the copy rate
 // What brought it there, at 8192 x 4096 x 6144: one CTA a tile, the accumulator
 // held while it was stored, 125 us; CTA pairs 111; outputs packed before the
@@ -66,6 +67,7 @@ constexpr int kXMaxSplits = 8;                   // the largest portable cluster
 // on an SM (228 KiB less 1 KiB a CTA; the static part is below 256 bytes).
 constexpr int kXMaxSmem = 227 * 1024 - 256;
 constexpr int kXSmemPair = 228 * 1024 / 2 - 1024 - 256;
+constexpr int kXFuseSmem = 256;                  // further barriers of a fused product
 
 struct MxGemmParams {
   int M, N, E;               // E = 0: dense
@@ -88,6 +90,11 @@ struct MxGemmParams {
   void* y;
   long long y_stride;
   uint32_t* status;
+  // FUSED: the unquantised rows
+  const uint8_t* x;
+  const int32_t* perm;
+  long long x_stride;        // bytes
+  int x_rows, x_dtype, x_wide, K;
 };
 
 // One stage: b codes, token codes, b scales, token scales.
@@ -95,6 +102,9 @@ __host__ __device__ constexpr int mx_stage_bytes(int nt) { return kXWBytes + nt 
 
 // Instruction descriptor: kind::mxf4, E2M1 x E2M1, UE8M0 scales, K-major
 // operands, M x N tile, the scales of byte pair `id` (0 or 2) of each word.
+// Fused: a stage holds b only; behind the stages, a's codes and scales of every K stage.
+constexpr int kXFuseStageBytes = kXWBytes + kXSfBytes;
+__host__ __device__ constexpr int mx_fused_a_bytes(int nt) { return nt * kXRowBytes + kXSfBytes; }
 NVDEV uint32_t idesc_mxf4(int M, int N, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
          (id << 29);
@@ -245,8 +255,59 @@ NVDEV void mx_store32(const MxGemmParams& p, const uint32_t* r, int m0, int cnt,
   }
 }
 
-// PLAIN: neither bias nor row weight.
-template <typename T, bool PLAIN>
+// FUSED: the epilogue's warps, idle until the accumulator is full, quantise
+// this CTA's share of K of every token into shared memory behind the stages:
+// for each K stage the codes as the TMA would put them (128-byte rows, 16-byte
+// chunk c of row r at c ^ (r & 7)), then for each K stage the scale atoms.
+// Units (stage, token, atom) go over the warps in that order; a stage's barrier
+// counts the warps.  A rolled loop without loads ahead: the passes are few, and
+// fetching straight-line code costs more than it saves (four passes at a time
+// with their loads first: 6.0 us for 1 x 1024 x 6144, one by one 5.4).
+constexpr int kXFuseTokens = 16;                 // rows of x that a product quantises itself, at most
+constexpr int kXFuseStages = 32;                 // and K stages of a CTA
+template <typename T> __host__ __device__ constexpr int fuse_pass() { return kXEpiWarps * 32 / unit_lanes<T>(); }
+template <typename T, bool WIDE>
+NVDEV void mx_quantize_tokens(const MxGemmParams& p, uint8_t* at_codes, uint8_t* at_scales, int kt0, int nkt,
+                              uint64_t* a_bar) {
+  constexpr int EPL = lane_elems<T>(), LPU = unit_lanes<T>(), kPass = fuse_pass<T>();
+  const int lane = threadIdx.x & 31, l = lane & (LPU - 1);
+  const int mine = ((threadIdx.x >> 5) - 2) * (32 / LPU) + lane / LPU;
+  const int per = 2 * p.M, units = nkt * per;                // units of a stage, of all
+  // u / per = u m >> 16, exact for u < 2^16 / per (here u < units + kPass)
+  static_assert((kXFuseStages * 2 * kXFuseTokens + fuse_pass<Bf16>()) * 2 * kXFuseTokens <= 65536, "unit division");
+  const uint32_t m = 65536u / (uint32_t)per + 1u;
+  const uint8_t* x_end = p.x + (size_t)(p.x_rows - 1) * (size_t)p.x_stride + (size_t)p.K * T::size;
+  int done = 0;                                              // stages handed over
+#pragma unroll 1
+  for (int first = 0; first < units; first += kPass) {
+    const int u = first + mine, i = (int)(((uint32_t)u * m) >> 16), r = u - i * per, row = r >> 1, atom = r & 1;
+    const int src = u >= units ? -1 : p.perm ? __ldg(p.perm + row) : row;
+    const int n = src >= 0 && src < p.x_rows ? p.K : 0;      // a row without a source reads as zeros
+    uint32_t w[8];
+    load_share<T, WIDE ? 16 : T::size>(p.x + (n ? (size_t)src * (size_t)p.x_stride : 0),
+                                       ((kt0 + i) * kXAtoms + atom) * kMxGroup + l * EPL, n, p.x, x_end, w);
+    uint32_t q[EPL / 8], sf;
+    mx_unit<T>(w, q, sf);
+    if (u < units) {
+      const int byte = atom * 64 + l * (EPL / 2);
+      uint8_t* dst = at_codes + (i * p.nt + row) * kXRowBytes + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
+      if constexpr (EPL == 16) *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = q[0];
+      if (l == 0) *reinterpret_cast<uint32_t*>(at_scales + i * kXSfBytes + atom * kAtomBytes + row * 16) = sf;
+    }
+    const int all = min(first + kPass, units);               // units that the warps have now
+    if ((done + 1) * per <= all) {
+      fence_proxy_async();                                   // the MMA reads through the async proxy
+      __syncwarp();
+      for (; (done + 1) * per <= all; ++done)
+        if (lane == 0) mbar_arrive(&a_bar[done]);
+    }
+  }
+}
+
+// PLAIN: neither bias nor row weight.  FUSED: a single tile a CTA, dense, its
+// tokens quantised here.
+template <typename T, bool PLAIN, bool FUSED>
 __global__ void __launch_bounds__(kXThreads, 2)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmX32, const MxGemmParams p) {
@@ -257,6 +318,7 @@ __global__ void __launch_bounds__(kXThreads, 2)
   __shared__ __align__(8) uint64_t acc_full_bar[2];
   __shared__ __align__(8) uint64_t acc_empty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t a_bar[FUSED ? kXFuseStages : 1];
   __shared__ uint32_t tmem_base_s;
   __shared__ int abort_s;
   volatile int* abort_flag = &abort_s;
@@ -269,8 +331,9 @@ __global__ void __launch_bounds__(kXThreads, 2)
   const int n_acc = p.n_acc;
   const uint32_t need = (uint32_t)(n_acc * nt_pad) + 4 * kXAtoms * 2;
   const uint32_t tcols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
-  const int stage_bytes = mx_stage_bytes(p.nt);
-  const int x_bytes = p.nt * kXRowBytes;                     // nt is a multiple of 16: whole 8-row swizzle groups
+  // (FUSED: a's codes and scales lie behind the stages, for all of K)
+  const int stage_bytes = FUSED ? kXFuseStageBytes : mx_stage_bytes(p.nt);
+  const int x_bytes = FUSED ? 0 : p.nt * kXRowBytes;         // nt is a multiple of 16: whole 8-row swizzle groups
   // this CTA's share of K
   const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
   const int kt0 = (int)((long long)p.kt_total * rank / p.splits);
@@ -286,13 +349,18 @@ __global__ void __launch_bounds__(kXThreads, 2)
       mbar_init(&acc_empty_bar[i], kXEpiWarps);
     }
     mbar_init(&drain_bar, 1);
+    if constexpr (FUSED) {
+      for (int i = 0; i < nkt; ++i) mbar_init(&a_bar[i], kXEpiWarps);
+    }
     abort_s = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmW);
-    prefetch_tmap(&tmX);
-    prefetch_tmap(&tmX32);
+    if constexpr (!FUSED) {
+      prefetch_tmap(&tmX);
+      prefetch_tmap(&tmX32);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&tmem_base_s, tcols);
@@ -364,15 +432,17 @@ __global__ void __launch_bounds__(kXThreads, 2)
           uint8_t* sX = smem + stage * stage_bytes + kXWBytes;
           uint8_t* sSFX = sX + x_bytes + kXSfBytes;
           const uint32_t sf_bytes = (uint32_t)min(kXAtoms, p.groups - kt * kXAtoms) * kAtomBytes;
-          mbar_arrive_expect_tx(&full_bar[stage], kXWBytes + xb + 2 * sf_bytes);
+          mbar_arrive_expect_tx(&full_bar[stage], kXWBytes + (FUSED ? sf_bytes : xb + 2 * sf_bytes));
           if (issued >= early) load_b(c.wt, c.e, kt, stage);
-          if (whole) {
+          if constexpr (FUSED) {
+          } else if (whole) {
             tma_load_2d(sX, &tmX, kt * kXRowBytes, c.row0, &full_bar[stage]);
           } else {
             for (int b = 0; b < boxes; ++b)
               tma_load_2d(sX + b * 32 * kXRowBytes, &tmX32, kt * kXRowBytes, c.row0 + 32 * b, &full_bar[stage]);
           }
-          bulk_load(sSFX, p.a_sf + (size_t)(c.row0 / kRowTile) * sf_tile + (size_t)kt * kXSfBytes, sf_bytes,
+          if constexpr (!FUSED)
+            bulk_load(sSFX, p.a_sf + (size_t)(c.row0 / kRowTile) * sf_tile + (size_t)kt * kXSfBytes, sf_bytes,
                     &full_bar[stage]);
         }
         __syncwarp();
@@ -397,9 +467,10 @@ __global__ void __launch_bounds__(kXThreads, 2)
     // a single divergent lane issues too slowly to keep the tensor pipe busy)
     const uint32_t elected = elect_one();
     const uint32_t s0 = smem_u32(smem);
-    const uint64_t w0 = sdesc_sw128(s0), x0 = sdesc_sw128(s0 + kXWBytes);
+    const uint32_t a_at = s0 + p.stages * stage_bytes;
+    const uint64_t w0 = sdesc_sw128(s0), x0 = sdesc_sw128(FUSED ? a_at : s0 + kXWBytes);
     const uint64_t sfw0 = sdesc_scale_atom(s0 + kXWBytes + x_bytes);
-    const uint64_t sfx0 = sdesc_scale_atom(s0 + kXWBytes + x_bytes + kXSfBytes);
+    const uint64_t sfx0 = sdesc_scale_atom(FUSED ? a_at + nkt * p.nt * kXRowBytes : s0 + kXWBytes + x_bytes + kXSfBytes);
     const uint64_t stage_step = (uint64_t)stage_bytes >> 4;
     constexpr uint64_t kAtomStep = kAtomBytes >> 4;
     const uint32_t sfw_t = tmem + (uint32_t)(n_acc * nt_pad), sfx_t = sfw_t + 4 * kXAtoms;
@@ -422,7 +493,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
       const uint32_t acc_t = tmem + (uint32_t)(buf * nt_pad);
       uint32_t accumulate = 0;
       for (int i = 0; i < nkt; ++i) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[stage], phase, abort_flag) &&
+                                         (!FUSED || mbar_wait(&a_bar[FUSED ? i : 0], 0, abort_flag)));
         if (!ok) {
           if (elected) {
             *abort_flag = 1;
@@ -433,6 +505,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
         const bool whole = p.groups - (kt0 + i) * kXAtoms >= kXAtoms;     // else K ends with one atom
         if (elected) {
           const uint64_t d = (uint64_t)stage * stage_step;
+          const uint64_t dx = FUSED ? (uint64_t)(i * p.nt * kXRowBytes >> 4) : d;
+          const uint64_t dsx = FUSED ? (uint64_t)(i * kXSfBytes >> 4) : d;
           // straight-line code for either length of a stage: a branch per
           // instruction would starve the tensor pipe
           auto issue = [&](auto n_atoms) {
@@ -440,11 +514,11 @@ __global__ void __launch_bounds__(kXThreads, 2)
 #pragma unroll
             for (int j = 0; j < A; ++j) {
               tc_cp_scale_atom(sfw_t + 4 * j, sfw0 + d + j * kAtomStep);
-              tc_cp_scale_atom(sfx_t + 4 * j, sfx0 + d + j * kAtomStep);
+              tc_cp_scale_atom(sfx_t + 4 * j, sfx0 + dsx + j * kAtomStep);
             }
 #pragma unroll
             for (int j = 0; j < 2 * A; ++j)          // 64 elements = 32 bytes of K per MMA, two per atom
-              mma_mxf4(acc_t, w0 + d + 2 * j, x0 + d + 2 * j, (j & 1) ? id2 : id0, sfw_t + 4 * (j >> 1),
+              mma_mxf4(acc_t, w0 + d + 2 * j, x0 + dx + 2 * j, (j & 1) ? id2 : id0, sfw_t + 4 * (j >> 1),
                        sfx_t + 4 * (j >> 1), accumulate | j);
           };
           if (whole) issue(std::integral_constant<int, kXAtoms>{});
@@ -481,6 +555,17 @@ __global__ void __launch_bounds__(kXThreads, 2)
     float* red = reinterpret_cast<float*>(smem);             // split K: [token][128], the idle stages
     int buf = 0;
     uint32_t acc_phase = 0;
+    if constexpr (FUSED) {
+      uint8_t* codes = smem + p.stages * stage_bytes;
+      uint8_t* scales = codes + nkt * p.nt * kXRowBytes;
+      auto quantize = [&](auto tag) {
+        if (p.x_wide) mx_quantize_tokens<decltype(tag), true>(p, codes, scales, kt0, nkt, a_bar);
+        else mx_quantize_tokens<decltype(tag), false>(p, codes, scales, kt0, nkt, a_bar);
+      };
+      if (p.x_dtype == MXFP4_DTYPE_BF16) quantize(Bf16{});
+      else if (p.x_dtype == MXFP4_DTYPE_F16) quantize(F16{});
+      else quantize(F32{});
+    }
     for (int t = t_first; t < num_tiles; t += t_step) {
       const MxTile c = mx_tile(p, segs, t);
       const int n = c.wt * kXBM + n_in;
@@ -896,7 +981,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
 // Opts a kernel into the largest dynamic shared memory, once per device.
 template <auto Kernel>
-static nvfp4_status opt_in_smem() {
+static nvfp4_status opt_in_smem(int bytes = kXMaxSmem) {
   static std::mutex mu;
   static bool done[64] = {};
   int dev = 0;
@@ -904,7 +989,7 @@ static nvfp4_status opt_in_smem() {
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 0 || dev >= 64 || !done[dev]) {
     NV_CHECK(check_cuda(cudaFuncSetAttribute((const void*)Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kXMaxSmem),
+                                             bytes),
                         "cudaFuncSetAttribute"));
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
@@ -921,6 +1006,12 @@ struct MxGemmArgs {
   long long y_stride = 0;
   uint32_t* status = nullptr;
   bool early_b = false;
+  // unquantised a, for a fused product (x_rows of them, x_stride elements apart)
+  const void* x = nullptr;
+  const int32_t* perm = nullptr;
+  int x_rows = 0, x_dtype = 0;
+  long long x_stride = 0;
+  bool x_wide = false;
 };
 
 // Tile width, pipeline depth and K splits of a product (host arithmetic).
@@ -985,12 +1076,45 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   return pl;
 }
 
-template <typename T, bool PLAIN>
+// The plan of a product that quantises its own tokens, from the plan of one
+// that does not; false where there is none or it would be slower.  It takes a
+// single token tile, a tile a CTA, and a's share of K beside three stages (four
+// where K is split) at least.  Every CTA converts the tokens for itself, which costs 0.4 us a pass
+// (32 units of 128 elements, 16 of fp32; more where rows are not 16-byte
+// aligned) where the quantiser's launch costs 2 on the GPU and 2.5 on the host.
+// Measured, tokens: us fused, us with the quantiser's kernel
+//   bf16  1024 x 6144 (6 stages a CTA)    1: 5.4, 7.2   8: 5.7, 7.4  16: 7.0, 7.6
+//         6144 x 6144 (8 stages)          1: 7.9, 9.5   8: 8.8, 9.9  12: 10.1, 10.0
+//         12288 x 4096 (16 stages)        1: 9.9, 11.0  6: 10.5, 11.1  8: 11.4, 11.1
+//         18000 x 6144 (24 stages)        1: 13.8, 15.1 4: 14.1, 15.1  6: 15.3, 15.2
+//         20000 x 5000 (20 stages; three in flight)                     1: 14.5, 14.9
+//         3000 x 20000 (20 stages, split; three in flight, not taken)   1: 12.9, 12.1
+//   fp32  6144 x 6144                     4: 8.7, 9.8   6: 9.7, 9.8    8: 10.8, 9.9
+//   rows at odd elements, 6144 x 6144     bf16 8: 9.3, 9.8  12: 11.0, 9.9
+//                                         fp32 4: 8.8, 9.8   6: 10.5, 9.9
+static bool fuse_quantiser(MxPlan& pl, int M, int N, int K, int E, bool wide, int dtype, int sms) {
+  if (E != 0 || pl.pair || M > kXFuseTokens) return false;
+  const long long ctas = (long long)(N + kXBM - 1) / kXBM * pl.splits;
+  const int kt = (mx_groups(K) + kXAtoms - 1) / kXAtoms, nkt = (kt + pl.splits - 1) / pl.splits;
+  if (ctas > 2ll * sms || nkt > kXFuseStages) return false;
+  const int pass = dtype == MXFP4_DTYPE_F32 ? fuse_pass<F32>() : fuse_pass<Bf16>();
+  if (nkt * 2 * M > pass * (wide ? 6 : 4)) return false;
+  const int per_sm = pl.splits > 1 || ctas > sms ? 2 : 1;    // (clusters fit at two CTAs an SM)
+  const int stages = ((per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - kXFuseSmem - nkt * mx_fused_a_bytes(pl.nt)) /
+                     kXFuseStageBytes;
+  if (stages < (pl.splits > 1 ? 4 : 3)) return false;
+  pl.ctas_per_sm = per_sm;
+  pl.n_acc = 1;
+  pl.stages = std::min(kXMaxStages, stages);
+  return true;
+}
+
+template <typename T, bool PLAIN, bool FUSED>
 static nvfp4_status run_mx_gemm(const MxPlan& pl, int sms, const CUtensorMap& tmW,
                                 const CUtensorMap& tmX, const CUtensorMap& tmX32, const MxGemmParams& p,
                                 long long tiles, cudaStream_t s) {
-  constexpr auto kernel = mx_gemm_kernel<T, PLAIN>;
-  NV_CHECK(opt_in_smem<kernel>());
+  constexpr auto kernel = mx_gemm_kernel<T, PLAIN, FUSED>;
+  NV_CHECK(opt_in_smem<kernel>(FUSED ? kXMaxSmem - kXFuseSmem : kXMaxSmem));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1007,7 +1131,9 @@ static nvfp4_status run_mx_gemm(const MxPlan& pl, int sms, const CUtensorMap& tm
   cfg.blockDim = dim3(kXThreads);
   cfg.gridDim = dim3((unsigned)(pl.splits > 1 ? tiles * pl.splits
                                               : std::max(1ll, std::min<long long>(tiles, (long long)sms * pl.ctas_per_sm))));
-  cfg.dynamicSmemBytes = (size_t)pl.stages * mx_stage_bytes(pl.nt) + mx_segment_bytes(p.E) + 1024;
+  cfg.dynamicSmemBytes = FUSED ? (size_t)pl.stages * kXFuseStageBytes +
+                                     (size_t)((p.kt_total + pl.splits - 1) / pl.splits) * mx_fused_a_bytes(pl.nt) + 1024
+                               : (size_t)pl.stages * mx_stage_bytes(pl.nt) + mx_segment_bytes(p.E) + 1024;
   cfg.stream = s;
   return check_cuda(cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, tmX32, p), "mx_gemm_kernel");
 }
@@ -1064,10 +1190,7 @@ static nvfp4_status with_output(const MxGemmArgs& a, F&& f) {
   return by_plain(F32{});
 }
 
-static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
-  int sms = 0;
-  NV_CHECK(device_sm_count(&sms));
-  const MxPlan pl = plan_mx_gemm(a.M, a.N, a.K, a.E, sms);
+static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, const MxPlan& pl, int sms, cudaStream_t s) {
   MxGemmParams p;
   p.M = a.M;
   p.N = a.N;
@@ -1093,6 +1216,7 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   p.y = a.y;
   p.y_stride = a.y_stride;
   p.status = a.status;
+  p.x = static_cast<const uint8_t*>(a.x);
   // tiles at most: each expert may end in a partly filled token tile
   const long long tiles = (long long)p.n_wt * (a.E ? (a.M + pl.nt - 1) / pl.nt + a.E : p.n_tt);
   const uint64_t inner = (uint64_t)mx_row_bytes(a.K);
@@ -1115,6 +1239,17 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
   CUtensorMap tmW, tmX, tmX32;
   NV_CHECK(make_tmap_2d(&tmW, a.b_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner,
                         (uint64_t)std::max(1, a.E) * (uint64_t)a.N, inner, kXRowBytes, kXBM));
+  if (a.x) {
+    p.perm = a.perm;
+    p.x_rows = a.x_rows;
+    p.x_dtype = a.x_dtype;
+    p.x_wide = a.x_wide;
+    p.K = a.K;
+    p.x_stride = a.x_stride * mx_elem_size(a.x_dtype);
+    return with_output(a, [&](auto tag, auto plain) -> nvfp4_status {
+      return run_mx_gemm<decltype(tag), decltype(plain)::value, true>(pl, sms, tmW, tmW, tmW, p, tiles, s);
+    });
+  }
   NV_CHECK(make_tmap_2d(&tmX, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, inner, (uint64_t)a.M, inner, kXRowBytes,
                         (uint32_t)pl.nt));
   if (a.E) {
@@ -1124,7 +1259,7 @@ static nvfp4_status launch_mx_gemm(const MxGemmArgs& a, cudaStream_t s) {
     tmX32 = tmX;
   }
   return with_output(a, [&](auto tag, auto plain) -> nvfp4_status {
-    return run_mx_gemm<decltype(tag), decltype(plain)::value>(pl, sms, tmW, tmX, tmX32, p, tiles, s);
+    return run_mx_gemm<decltype(tag), decltype(plain)::value, false>(pl, sms, tmW, tmX, tmX32, p, tiles, s);
   });
 }
 
@@ -1183,7 +1318,18 @@ extern "C" nvfp4_status mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_sc
   g.row_weight = row_weight; g.bias = bias;
   g.out_dtype = out_dtype; g.y = y; g.y_stride = y_stride;
   g.status = static_cast<uint32_t*>(ws);
-  return launch_mx_gemm(g, as_stream(stream));
+  int sms = 0;
+  NV_CHECK(device_sm_count(&sms));
+  return launch_mx_gemm(g, plan_mx_gemm(M, N, K, E, sms), sms, as_stream(stream));
+}
+
+// Whether the memory from the first to the last element of two matrices meets.
+static bool overlap(const void* a, int a_rows, long long a_stride, int a_cols, int a_elem, const void* b, int b_rows,
+                    long long b_stride, int b_cols, int b_elem) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + ((uintptr_t)(a_rows > 1 ? (a_rows - 1) * a_stride : 0) + (uintptr_t)a_cols) * a_elem;
+  const uintptr_t b1 = b0 + ((uintptr_t)(b_rows > 1 ? (b_rows - 1) * b_stride : 0) + (uintptr_t)b_cols) * b_elem;
+  return a0 < b1 && b0 < a1;
 }
 
 struct MxLinearScratch {
@@ -1229,13 +1375,29 @@ extern "C" nvfp4_status mxfp4_linear(const void* x, int dtype, int rows, long lo
   g.row_weight = row_weight; g.bias = bias;
   g.out_dtype = out_dtype; g.y = y; g.y_stride = y_stride;
   g.status = l.status;
+  int sms = 0;
+  NV_CHECK(device_sm_count(&sms));
+  MxPlan pl = plan_mx_gemm(M, N, K, E, sms);
+  cudaStream_t s = as_stream(stream);
+  // (a fused product reads x while it writes y)
+  const int elem = mx_elem_size(dtype);
+  const bool wide = row_access_bytes(x, rows > 1 ? row_stride * elem : 0, elem) >= 16;
+  if (rows > 0 && !overlap(x, rows, row_stride, K, elem, y, M, y_stride, N, mx_elem_size(out_dtype)) &&
+      fuse_quantiser(pl, M, N, K, E, wide, dtype, sms)) {
+    g.x = x;
+    g.perm = perm;
+    g.x_rows = rows;
+    g.x_dtype = dtype;
+    g.x_stride = row_stride;
+    g.x_wide = wide;
+    return launch_mx_gemm(g, pl, sms, s);
+  }
   // b may load before the quantiser has finished: the quantiser itself starts
   // only behind everything queued earlier, which may have written b
   g.early_b = true;
-  cudaStream_t s = as_stream(stream);
   NV_CHECK(launch_mx_quantize(x, dtype, rows, K, row_stride, perm, M, NVFP4_LAYOUT_TILED, l.codes, l.scales, s,
                               expert_offsets, expert_counts, E));
-  return launch_mx_gemm(g, s);
+  return launch_mx_gemm(g, pl, sms, s);
 }
 
 extern "C" int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages) {
@@ -1245,4 +1407,13 @@ extern "C" int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, in
   if (pair) *pair = pl.pair ? 1 : 0;
   if (stages) *stages = pl.stages;
   return pl.nt;
+}
+
+extern "C" int nvfp4_test_mxfp4_fuses(int M, int N, int K, int dtype, int wide, int* stages, int* ctas_per_sm) {
+  if (M < 1 || N < 1 || K < 1 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30) || !mx_dtype_ok(dtype)) return -1;
+  MxPlan pl = plan_mx_gemm(M, N, K, 0, 148);
+  if (!fuse_quantiser(pl, M, N, K, 0, wide != 0, dtype, 148)) return 0;
+  if (stages) *stages = pl.stages;
+  if (ctas_per_sm) *ctas_per_sm = pl.ctas_per_sm;
+  return 1;
 }

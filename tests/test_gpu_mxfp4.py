@@ -354,6 +354,82 @@ def test_linear_is_quantize_then_matmul():
         assert not yp[perm < 0].any()
 
 
+# (M, N, K): products that quantise their rows themselves; whole and partial K
+# stages, one to four K splits, one and two CTAs an SM, rings that wrap
+FUSED = [(1, 1, 1), (1, 128, 32), (2, 500, 31), (3, 501, 201), (5, 300, 257), (16, 130, 300), (13, 640, 64),
+         (8, 1024, 6144), (7, 5001, 2010), (2, 12288, 4096), (1, 37000, 1000), (1, 1000, 8192), (1, 3000, 14000)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K", FUSED)
+def test_linear_of_few_rows(M, N, K, dtype):
+    """The product that quantises its rows itself: the values of the oracle,
+    and bit for bit those of quantising first; rows at every alignment, gathered
+    rows, rows without a source, blocks that are zero, NaN or infinite."""
+    require_cuda()
+    c = capi()
+    dt = DTYPES[dtype]
+    w, wv = operand(N, K, M + K)
+    bias = torch.randn(N, device="cuda")
+    rw = torch.randn(M, device="cuda")
+    for off in (0, 1, 8):
+        wide = off * dt.itemsize % 16 == 0
+        if c.nvfp4_test_mxfp4_fuses(M, N, K, dt, wide) is None:
+            assert dt == torch.float32 and M > 4 or not wide          # more passes over the rows
+            continue
+        base = matrix(M, (K + off + 15) // 16 * 16, dt, seed=off, special=False).cuda()
+        base[:, :off] = base[:, off + K:] = float("nan")               # the neighbours of x in memory
+        x = base[:, off:off + K]
+        if M > 2:
+            x[1, K // 2] = 0.0 if off else float("inf")
+            x[2] = 0.0
+        y = c.mxfp4_linear(x, w, out_dtype=torch.float32)
+        assert torch.equal(y.isnan(), c.mxfp4_matmul(c.mxfp4_quantize(x), w, out_dtype=torch.float32).isnan())
+        codes, scales = mxfp4.quantize(np64(x))
+        xv = mxfp4.dequantize(codes, scales, K)
+        good = np.isfinite(xv).all(axis=1)
+        ref = xv[good] @ wv.T
+        assert (np.abs(np64(y)[good] - ref) <= product_bound(xv[good], wv, ref, torch.float32)).all()
+        assert torch.isnan(y[torch.from_numpy(~good).cuda()]).all()
+        out = torch.full((M, N + 3), 7.0, dtype=dt, device="cuda")[:, 1:1 + N]
+        c.mxfp4_linear(x, w, out=out, bias=bias, row_weight=rw)
+        want = torch.full_like(out, 7.0)
+        c.mxfp4_matmul(c.mxfp4_quantize(x), w, out=want, bias=bias, row_weight=rw)
+        assert torch.equal(out.nan_to_num(5.0), want.nan_to_num(5.0))
+        perm = torch.randint(-2, 2 * M, (M,), dtype=torch.int32, device="cuda")
+        yp = c.mxfp4_linear(x, w, perm=perm)
+        assert torch.equal(yp.nan_to_num(5.0), c.mxfp4_matmul(c.mxfp4_quantize(x, perm=perm), w, out_dtype=dt).nan_to_num(5.0))
+        assert not yp[(perm < 0) | (perm >= M)].any()
+
+
+def test_few_rows_gathered_from_many_and_none():
+    require_cuda()
+    c = capi()
+    w, _ = operand(384, 600, 8)
+    assert c.nvfp4_test_mxfp4_fuses(4, 384, 600, torch.bfloat16)
+    x = matrix(5000, 600, torch.bfloat16, special=False).cuda()
+    perm = torch.tensor([4999, 17, 17, 5000], dtype=torch.int32, device="cuda")
+    y = c.mxfp4_linear(x, w, perm=perm)
+    assert torch.equal(y, c.mxfp4_matmul(c.mxfp4_quantize(x, perm=perm), w))
+    assert torch.equal(y[1], y[2]) and not y[3].any()
+    assert not c.mxfp4_linear(x[:0], w, perm=perm).any()
+
+
+def test_y_in_the_place_of_few_rows():
+    """y over x, and y whose rows lie between x's: x is read before y is written."""
+    require_cuda()
+    c = capi()
+    w, _ = operand(512, 512, 3)
+    assert c.nvfp4_test_mxfp4_fuses(4, 512, 512, torch.bfloat16)
+    both = torch.cat([matrix(4, 512, torch.bfloat16, seed=i, special=False) for i in (1, 2)], dim=1).cuda()
+    x = both[:, :512]
+    want = c.mxfp4_linear(x.clone(), w)
+    assert torch.equal(c.mxfp4_linear(x, w, out=both[:, 512:]), want)
+    for shift in (0, 1):                          # rows shifted by one: y's row i is x's row i + 1
+        z = torch.cat([x, x[:1]])
+        assert torch.equal(c.mxfp4_linear(z[:4], w, out=z[shift:4 + shift]), want)
+
+
 @pytest.mark.parametrize("with_counts", [True, False])
 def test_grouped_linear_with_padding_rows(with_counts):
     """Rows of perm without a source: inside an expert's tokens they are

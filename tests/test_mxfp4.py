@@ -196,6 +196,35 @@ def test_product_plans():
             plan(*bad)
 
 
+def test_products_that_quantise_their_rows():
+    """Host arithmetic: shared memory and tiles of a fused mxfp4_linear fit."""
+    c = capi()
+    fuses = c.nvfp4_test_mxfp4_fuses
+    seen = 0
+    for M in (1, 2, 3, 5, 8, 12, 15, 16, 17, 64):
+        for N in (1, 128, 1000, 1024, 6144, 12288, 18000, 18944, 37888, 100000):
+            for K in (1, 32, 256, 257, 300, 2010, 2048, 4096, 6144, 8192, 16384, 1 << 20):
+                for dt in (torch.bfloat16, torch.float16, torch.float32):
+                    for wide in (True, False):
+                        f = fuses(M, N, K, dt, wide)
+                        if f is None:
+                            continue
+                        seen += 1
+                        stages, per_sm = f
+                        nt, splits, pair, _ = c.nvfp4_test_mxfp4_plan(M, N, K)
+                        share = -(-(-(-K // 256)) // splits)           # K stages of a CTA
+                        assert M <= 16 and nt == 16 and not pair and 3 <= stages <= 8 and share <= 32
+                        assert -(-N // 128) * splits <= 148 * per_sm
+                        smem = stages * 17408 + share * (16 * 128 + 1024) + 1024
+                        assert smem <= (227 * 1024 - 512 if per_sm == 1 else 228 * 512 - 1024 - 512)
+                        assert nt * 512 <= stages * 17408              # the split's partial sums
+    assert seen > 500
+    for M, N, K in ((17, 1024, 6144), (16, 6144, 6144), (1, 100000, 512), (1, 128, 1 << 20)):
+        assert fuses(M, N, K, torch.bfloat16) is None
+    with pytest.raises(ValueError):
+        fuses(0, 1, 1, torch.float32)
+
+
 def test_balance_refusals():
     lib = capi().lib
 
