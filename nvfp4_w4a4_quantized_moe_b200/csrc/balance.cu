@@ -13,15 +13,23 @@
 // Backward, one kernel: the same row arithmetic, with the experts' shares f
 // of the row's sequence held in registers while the sequence lasts.
 //
-// Bound: HBM (logits in; gradient out), with one exponential (softmax) or one
-// exponential and one reciprocal (sigmoid) per element behind it; below some
-// ten thousand tokens the chain of loads, joins and launches.  Measured on one
-// B200 (fp32, 128 experts, top-8): 262,144 tokens forward 38 us (3.7 TB/s),
-// backward 50 us (5.3 TB/s); 65,536 tokens 19 and 14 us (inputs in L2); 16
-// tokens of 80 experts 3.8 and 2.7 us.  With four logits a lane and row instead of
-// sixteen (five shuffles for each maximum and sum), a reciprocal a logit for
-// softmax too and the choices counted before the rows, 65,536 tokens took 57
-// and 31 us.
+// Bound: HBM (logits in; gradient out) behind a dozen instructions an element,
+// one exponential (softmax) or one exponential and one reciprocal (sigmoid)
+// among them; below some ten thousand tokens the chain of loads, joins and
+// launches.  Measured on one B200 (128 experts, top-8, softmax, us forward and
+// backward, logits from HBM):
+//                                        fp32          bf16
+//   262,144 tokens, 33 sequences, mask   38.9, 50.7    36.4, 36.5
+//   65,531 tokens, 17 sequences, mask    20.0, 15.7    18.9, 13.1
+//   65,531 tokens, one sequence          15.9, 15.2    15.2, 11.7
+//   4,096 tokens, one sequence            8.6,  3.1     8.4,  3.1
+//   16 tokens of 80 experts               3.3,  2.5     3.3,  2.5
+// What brought it there: four logits a lane and row (five shuffles for each
+// maximum and sum), a reciprocal a logit for softmax too and the choices counted
+// before the rows, 57 and 31 us at 65,536 tokens fp32; sixteen a lane 23 and 17
+// (bf16 22 and 16: 433 instructions a warp's row group); pairs of fp32 in one
+// instruction, one fused operation before an exponential, loads without
+// branches, a row ahead, and smaller blocks of the finish, the table above.
 #include <algorithm>
 #include <type_traits>
 
@@ -57,38 +65,76 @@ NVDEV int seq_of(const BalanceShape& b, int t) {
   return lo;
 }
 
-// Four neighbouring logits from element e of a row; -inf past E.
-template <typename T, bool VEC>
-NVDEV void load4(const void* logits, long long row, int e, int E, bool live, float* v) {
+// A lane's share of a row: V quads of neighbouring logits, quad i from element
+// (i L + l) 4 on, as they are in memory.  Every lane loads, without a branch:
+// past the row's end from inside it (row_values puts -inf there).
+template <typename T, int V> struct RowWords { uint32_t w[V * T::size]; };
+template <typename T, bool VEC, int V>
+NVDEV void load_row(const uint8_t* row, int l, int L, int E, RowWords<T, V>& r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = -INFINITY;
-  if (!live || e >= E) return;
-  if constexpr (VEC) {
-    if constexpr (T::size == 4) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e));
-      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + row + e));
-      v[0] = T::lo(u.x); v[1] = T::hi(u.x); v[2] = T::lo(u.y); v[3] = T::hi(u.y);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e + i < E) {
-        if constexpr (T::size == 4) v[i] = __ldg(static_cast<const float*>(logits) + row + e + i);
-        else v[i] = T::from(__ldg(static_cast<const uint16_t*>(logits) + row + e + i));
+  for (int i = 0; i < V; ++i) {
+    const int e = (i * L + l) * 4;
+    if constexpr (VEC) {
+      const uint8_t* p = row + min(e, E - 4) * T::size;
+      if constexpr (T::size == 4) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+        r.w[4 * i] = u.x; r.w[4 * i + 1] = u.y; r.w[4 * i + 2] = u.z; r.w[4 * i + 3] = u.w;
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        r.w[2 * i] = u.x; r.w[2 * i + 1] = u.y;
       }
+    } else if constexpr (T::size == 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = __ldg(reinterpret_cast<const uint32_t*>(row) + min(e + j, E - 1));
+    } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        r.w[2 * i + j] = (uint32_t)__ldg(p + min(e + 2 * j, E - 1)) | ((uint32_t)__ldg(p + min(e + 2 * j + 1, E - 1)) << 16);
+    }
+  }
+}
+// Its values in pairs (packed fp32 instructions take two at once).
+template <typename T, int V>
+NVDEV void row_values(const RowWords<T, V>& r, int l, int L, int E, uint64_t* v) {
+#pragma unroll
+  for (int i = 0; i < V * 2; ++i) {
+    if constexpr (T::size == 4) v[i] = pack_f32x2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    else v[i] = pack_f32x2(T::lo(r.w[i]), T::hi(r.w[i]));
+  }
+  if (V * 4 * L != E) {
+#pragma unroll
+    for (int i = 0; i < V * 2; ++i) {
+      const int e = ((i >> 1) * L + l) * 4 + (i & 1) * 2;
+      v[i] = pack_f32x2(e < E ? lo_f32(v[i]) : -INFINITY, e + 1 < E ? hi_f32(v[i]) : -INFINITY);
+    }
   }
 }
 
-template <int N>
-NVDEV float row_max(const float* v, int lanes) {
-  float m = v[0];
+// Over the L lanes of a row.
+NVDEV float group_max(float m, int L) {
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-  for (int o = lanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < L) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
+NVDEV float group_sum(float z, int L) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < L) z += __shfl_xor_sync(0xffffffffu, z, o);
+  return z;
+}
+NVDEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+NVDEV uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+NVDEV uint64_t twice(float a) { return pack_f32x2(a, a); }
 NVDEV float ex2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -103,9 +149,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // l -> the row's scores up to a common factor (in place): exp(l - max), or
 // sigma(l), and where asked d = dlog(score)/dl (1, or sigma(-l)).
-// Softmax: exp2((l - max) log2(e)), whose two roundings move a share p by about
-// |log p| 2^-23 relative.  (The difference comes first: l log2(e) of the
-// type's lowest value, a usual mask, is no fp32 number.)
+// Softmax: exp2(l log2(e) - max log2(e)) in one fused operation an element.
+// The rounding of max log2(e) is a common factor of the row (below 2^0.01 while
+// |max| < 65536) and leaves the shares; the other moves a share p by about
+// |log p| 2^-24 relative.  Beyond that, and for a row whose max is no number,
+// exp2((l - max) log2(e)): l log2(e) of the type's lowest value, a usual mask,
+// is no fp32 number, and is 0 in either form.
 // Sigmoid: while the row's largest logit is above -60 the sigmas are taken as
 // they are (one that underflows is below 1e-12 of the largest); below it
 // sigma(l) is exp(l) to the last bit of fp32, and the shares are a softmax,
@@ -114,22 +163,39 @@ constexpr float kLog2e = 1.4426950408889634f;
 // -inf (a masked expert, or past E) gives 0 by itself; a row of nothing else
 // has max = -inf and is measured from 0 instead.
 template <int N, int SCORE, bool GRAD>
-NVDEV void row_scores(float* l, float* d, int lanes) {
-  const float m = row_max<N>(l, lanes);
-  if (SCORE == MOE_BALANCE_SOFTMAX || m < -60.0f) {
-    const float from = m == -INFINITY ? 0.0f : m;
+NVDEV void row_scores(uint64_t* l, uint64_t* d, int L) {
+  float m = fmaxf(lo_f32(l[0]), hi_f32(l[0]));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      l[i] = ex2_approx((l[i] - from) * kLog2e);
-      if (GRAD) d[i] = 1.0f;
+  for (int i = 1; i < N; ++i) m = fmaxf(m, fmaxf(lo_f32(l[i]), hi_f32(l[i])));
+  m = group_max(m, L);
+  if (SCORE == MOE_BALANCE_SOFTMAX || m < -60.0f) {
+    if (fabsf(m) < 65536.0f) {
+      const uint64_t by = twice(kLog2e), from = twice(-m * kLog2e);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t x = fma_f32x2(l[i], by, from);
+        l[i] = pack_f32x2(ex2_approx(lo_f32(x)), ex2_approx(hi_f32(x)));
+      }
+    } else {
+      const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        l[i] = pack_f32x2(ex2_approx((lo_f32(l[i]) - from) * kLog2e), ex2_approx((hi_f32(l[i]) - from) * kLog2e));
+    }
+    if (GRAD && SCORE != MOE_BALANCE_SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = twice(1.0f);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float t = ex2_approx(-l[i] * kLog2e);
-      const float sg = rcp_approx(1.0f + t);
-      if (GRAD) d[i] = l[i] < 0.0f ? 1.0f - sg : t * sg;
-      l[i] = sg;
+      const uint64_t x = mul_f32x2(l[i], twice(-kLog2e));
+      const uint64_t t = pack_f32x2(ex2_approx(lo_f32(x)), ex2_approx(hi_f32(x)));
+      const uint64_t t1 = add_f32x2(t, twice(1.0f));
+      const float s0 = rcp_approx(lo_f32(t1)), s1 = rcp_approx(hi_f32(t1));
+      if (GRAD)
+        d[i] = pack_f32x2(lo_f32(l[i]) < 0.0f ? 1.0f - s0 : lo_f32(t) * s0, hi_f32(l[i]) < 0.0f ? 1.0f - s1 : hi_f32(t) * s1);
+      l[i] = pack_f32x2(s0, s1);
     }
   }
   __syncwarp();
@@ -155,10 +221,15 @@ struct BalanceOut {
   float* probs;       // [S][E]
 };
 
-// V x 4 logits a lane; UR rows in flight per group of lanes.  ONE: a single
+// Whether the forward's registers hold the next rows beside those at work: 32
+// words of a row do not fit (32768 x 1024 fp32: 60.4 us ahead, 46.2 not), nor
+// do 16 with the addresses of single elements (65536 x 127 fp32: 25.1, 21.6).
+template <typename T, bool VEC, int V> constexpr bool loads_ahead() { return T::size == 2 || (VEC && V <= 4); }
+
+// V x 4 logits a lane; UR rows at once per group of lanes.  ONE: a single
 // block takes every token (chunk >= T) and writes the results itself.
 template <typename T, bool VEC, int V, int UR, int SCORE, bool ONE>
-__global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kBalThreads, ONE ? 1 : V <= 4 ? 3 : 2)
     balance_pieces_kernel(const void* __restrict__ logits, const int32_t* __restrict__ topk_idx, const BalanceShape b,
                           int chunk, const BalancePieces out, const BalanceOut res) {
   extern __shared__ float s_sum[];                          // [warps][E], then int counts [E]
@@ -185,46 +256,78 @@ __global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2)
     if (threadIdx.x == 0) s_tokens = 0;
     __syncthreads();
     int kept = 0;
-    float acc[V * 4];
+    uint64_t acc2[V * 2];
 #pragma unroll
-    for (int i = 0; i < V * 4; ++i) acc[i] = 0.0f;
-    for (int base = r0 + warp * G; base < r1; base += kBalWarps * G * UR) {
-      float v[UR][V * 4];
-      int choice[UR];
-      bool live[UR];
+    for (int i = 0; i < V * 2; ++i) acc2[i] = 0;
+    // the next rows load while these are worked on
+    RowWords<T, V> w[2][UR];
+    int choice[2][UR];
+    bool live[2][UR];
+    auto load = [&](auto buf, int base) {
+      constexpr int B = decltype(buf)::value;
 #pragma unroll
       for (int u = 0; u < UR; ++u) {
-        const int t = base + u * kBalWarps * G + g;
-        live[u] = t < r1;
+        const int t = base + u * kBalWarps * G + g, at = min(t, r1 - 1);
         // a masked token's logits are read, so that no load waits for the mask, and not used
-        const uint8_t m = live[u] && b.mask ? __ldg(b.mask + t) : 1;
-        choice[u] = live[u] && l < b.k ? __ldg(topk_idx + (size_t)t * b.k + l) : -1;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          load4<T, VEC>(logits, (long long)t * b.stride, (i * L + l) * 4, b.E, live[u], v[u] + 4 * i);
-        live[u] = live[u] && m;
+        const uint8_t m = b.mask ? __ldg(b.mask + at) : 1;
+        choice[B][u] = l < b.k ? __ldg(topk_idx + (size_t)at * b.k + l) : -1;
+        load_row<T, VEC, V>(static_cast<const uint8_t*>(logits) + (size_t)at * (size_t)b.stride * T::size, l, L, b.E,
+                            w[B][u]);
+        live[B][u] = t < r1 && m;
       }
+    };
+    auto work = [&](auto buf, int base) {
+      constexpr int B = decltype(buf)::value;
 #pragma unroll
       for (int u = 0; u < UR; ++u) {
-        row_scores<V * 4, SCORE, false>(v[u], nullptr, L);
-        float z = 0.0f;
+        uint64_t v[V * 2];
+        row_values<T, V>(w[B][u], l, L, b.E, v);
+        row_scores<V * 2, SCORE, false>(v, nullptr, L);
+        uint64_t z2 = v[0];
 #pragma unroll
-        for (int i = 0; i < V * 4; ++i) z += v[u][i];
-        for (int o = L >> 1; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (live[u]) {
-          const float inv = share_factor(z);
+        for (int i = 1; i < V * 2; ++i) z2 = add_f32x2(z2, v[i]);
+        const float z = group_sum(lo_f32(z2) + hi_f32(z2), L);
+        if (live[B][u]) {
+          const uint64_t inv = twice(share_factor(z));
 #pragma unroll
-          for (int i = 0; i < V * 4; ++i) acc[i] = __fmaf_rn(v[u][i], inv, acc[i]);
+          for (int i = 0; i < V * 2; ++i) acc2[i] = fma_f32x2(v[i], inv, acc2[i]);
           // the choices: integer atomics, whose order does not matter
-          if (choice[u] >= 0 && choice[u] < b.E) atomicAdd(&s_cnt[choice[u]], 1);
+          if ((unsigned)choice[B][u] < (unsigned)b.E) atomicAdd(&s_cnt[choice[B][u]], 1);
           for (int j = l + L; j < b.k; j += L) {
             const int e = __ldg(topk_idx + (size_t)(base + u * kBalWarps * G + g) * b.k + j);
-            if (e >= 0 && e < b.E) atomicAdd(&s_cnt[e], 1);
+            if ((unsigned)e < (unsigned)b.E) atomicAdd(&s_cnt[e], 1);
           }
           if (l == 0) ++kept;
         }
         __syncwarp();
       }
+    };
+    using B0 = std::integral_constant<int, 0>;
+    using B1 = std::integral_constant<int, 1>;
+    const int step = kBalWarps * G * UR;
+    int base = r0 + warp * G;
+    if constexpr (loads_ahead<T, VEC, V>() || ONE) {
+      if (base < r1) load(B0{}, base);
+#pragma unroll 1
+      for (; base < r1; base += 2 * step) {
+        if (base + step < r1) load(B1{}, base + step);
+        work(B0{}, base);
+        if (base + step >= r1) break;
+        if (base + 2 * step < r1) load(B0{}, base + 2 * step);
+        work(B1{}, base + step);
+      }
+    } else {
+#pragma unroll 1
+      for (; base < r1; base += step) {
+        load(B0{}, base);
+        work(B0{}, base);
+      }
+    }
+    float acc[V * 4];
+#pragma unroll
+    for (int i = 0; i < V * 2; ++i) {
+      acc[2 * i] = lo_f32(acc2[i]);
+      acc[2 * i + 1] = hi_f32(acc2[i]);
     }
     // lanes of the warp that hold the same experts, then the warps in order
 #pragma unroll
@@ -273,70 +376,78 @@ __global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2)
   }
 }
 
-// One block per (sequence, 32 experts): warp w adds pieces w, w + 32, ...,
-// eight loads in flight; the warps' sums join in warp order.
-constexpr int kFinThreads = 1024, kFinWarps = kFinThreads / 32;
+// One block per (sequence, FE experts): a group of FE lanes adds every
+// (256 / FE)-th piece, sixteen loads of each kind in flight; groups and warps
+// join in a fixed order.
+constexpr int kFinThreads = 256, kFinWarps = kFinThreads / 32, kFinLoads = 16;
+template <int kFinE>
 __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalanceShape b, int chunk,
                                                                      const BalancePieces in, double* __restrict__ dots,
                                                                      const BalanceOut res) {
-  __shared__ double s_p[kFinWarps][33];                     // padded: read by columns
-  __shared__ int32_t s_c[kFinWarps][33];
-  __shared__ int s_n[kFinWarps];
+  constexpr int kFinSlots = kFinThreads / kFinE;
+  __shared__ double s_p[kFinWarps][kFinE];
+  __shared__ int s_c[kFinWarps][kFinE], s_n[kFinWarps];
   __shared__ bool s_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int eg = gridDim.y, s = blockIdx.x, le = lane & (kFinE - 1), e = blockIdx.y * kFinE + le;
+  const int slot = threadIdx.x / kFinE;
+  // (the previous kernel ran behind whatever wrote the offsets)
+  const int r0 = seq_begin(b, s), r1 = seq_begin(b, s + 1);
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int eg = gridDim.y, s = blockIdx.x, e = blockIdx.y * 32 + lane;
-  const int r0 = seq_begin(b, s), r1 = seq_begin(b, s + 1);
   double p = 0.0;
   int c = 0, n = 0;
   if (r0 < r1) {
     const int first = r0 / chunk, last = (r1 - 1) / chunk;
-    for (int i0 = first + warp; i0 <= last; i0 += kFinWarps * 8) {
-      float vp[8];
-      int vc[8], vn[8];
+    for (int i0 = first + slot; i0 <= last; i0 += kFinSlots * kFinLoads) {
+      float vp[kFinLoads];
+      int vc[kFinLoads], vn[kFinLoads];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * kFinWarps;
-        const size_t piece = (size_t)min(i, last) + s;
-        const bool in_range = i <= last;
-        vp[u] = in_range && e < b.E ? in.probs[piece * b.E + e] : 0.0f;
-        vc[u] = in_range && e < b.E ? in.counts[piece * b.E + e] : 0;
-        vn[u] = in_range ? in.tokens[piece] : 0;             // the same in every lane
+      for (int u = 0; u < kFinLoads; ++u) {
+        const int i = i0 + u * kFinSlots;
+        const size_t piece = (size_t)i + s;
+        vp[u] = i <= last && e < b.E ? in.probs[piece * b.E + e] : 0.0f;
+        vc[u] = i <= last && e < b.E ? in.counts[piece * b.E + e] : 0;
+        vn[u] = i <= last ? in.tokens[piece] : 0;            // the same in the group's lanes
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kFinLoads; ++u) {
         p += (double)vp[u];
         c += vc[u];
         n += vn[u];
       }
     }
   }
-  s_p[warp][lane] = p;
-  s_c[warp][lane] = c;
-  if (lane == 0) s_n[warp] = n;
-  __syncthreads();
-  // warp w now joins expert w's 32 partial sums, in the same tree every time
-  p = s_p[lane][warp];
-  c = __reduce_add_sync(0xffffffffu, s_c[lane][warp]);
-  n = __reduce_add_sync(0xffffffffu, s_n[lane]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
-  __syncthreads();
-  if (lane == 0) {
-    const int e = blockIdx.y * 32 + warp;
-    const float mean = n > 0 ? (float)p / (float)n : 0.0f;
-    if (e < b.E) {
-      res.counts[(size_t)s * b.E + e] = c;
-      res.probs[(size_t)s * b.E + e] = mean;
-    }
-    s_p[0][warp] = n > 0 ? (double)((float)c * share_unit(b, n) * mean) : 0.0;
+  for (int o = kFinE; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(0xffffffffu, p, o);
+    c += __shfl_xor_sync(0xffffffffu, c, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (lane < kFinE) {
+    s_p[warp][lane] = p;
+    s_c[warp][lane] = c;
+    if (lane == 0) s_n[warp] = n;
   }
   __syncthreads();
   if (warp == 0) {
-    double dot = s_p[0][lane];
+    p = 0.0;
+    c = n = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    for (int w = 0; w < kFinWarps; ++w) {
+      p += s_p[w][le];
+      c += s_c[w][le];
+      n += s_n[w];
+    }
+    const float mean = n > 0 ? (float)p / (float)n : 0.0f;
+    const bool mine = lane < kFinE && e < b.E;
+    if (mine) {
+      res.counts[(size_t)s * b.E + e] = c;
+      res.probs[(size_t)s * b.E + e] = mean;
+    }
+    double dot = mine && n > 0 ? (double)((float)c * share_unit(b, n) * mean) : 0.0;
+#pragma unroll
+    for (int o = kFinE / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) {
       dots[(size_t)s * eg + blockIdx.y] = dot;
       if (blockIdx.y == 0) res.tokens[s] = n;
@@ -352,9 +463,9 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
   int full = 0;
   for (long long i = threadIdx.x; i < (long long)b.S * eg; i += kFinThreads) z += __ldcg(dots + i);
   for (int i = threadIdx.x; i < b.S; i += kFinThreads) full += __ldcg(res.tokens + i) > 0;
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   full = __reduce_add_sync(0xffffffffu, full);
-  __syncthreads();
   if (lane == 0) {
     s_p[warp][0] = z;
     s_n[warp] = full;
@@ -372,14 +483,16 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
   }
 }
 
+// Blocks per SM of the backward: fp32 rows in two buffers, their shares and
+// derivatives take more than the 80 registers that three leave (two against
+// three at 65,531 x 128 fp32: softmax 15.6 and 16.9 us, sigmoid 16.5 and 18.7;
+// bf16 at 262,144 x 128: 39.5 and 36.5).
+constexpr int balance_backward_blocks(int v, int size) { return v <= 4 && size == 2 ? 3 : 2; }
 template <typename T, bool VEC, int V, int UR, int SCORE>
-__global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2) balance_backward_kernel(const void* __restrict__ logits,
-                                                                       const BalanceShape b, int rows_per_warp,
-                                                                       float coeff, const int32_t* __restrict__ counts,
-                                                                       const int32_t* __restrict__ tokens,
-                                                                       const float* __restrict__ grad_loss,
-                                                                       void* __restrict__ dlogits,
-                                                                       long long grad_stride) {
+__global__ void __launch_bounds__(kBalThreads, balance_backward_blocks(V, T::size))
+    balance_backward_kernel(const void* __restrict__ logits, const BalanceShape b, int rows_per_warp, float coeff,
+                            const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
+                            const float* __restrict__ grad_loss, void* __restrict__ dlogits, long long grad_stride) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -391,9 +504,10 @@ __global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2) balance_backward_
   const int full = tokens[b.S];
   // this group's sequence: the tokens [s0, s1) that its shares f hold for
   int s0 = 0, s1 = 0;
-  float f[V * 4], scale = 0.0f;
+  float scale = 0.0f;
+  uint64_t f[V * 2];
 #pragma unroll
-  for (int i = 0; i < V * 4; ++i) f[i] = 0.0f;
+  for (int i = 0; i < V * 2; ++i) f[i] = 0;
   auto enter = [&](int t) {
     const int s = seq_of(b, t);
     scale = 0.0f;
@@ -411,69 +525,93 @@ __global__ void __launch_bounds__(kBalThreads, V <= 4 ? 3 : 2) balance_backward_
       const float unit = n > 0 ? share_unit(b, n) : 0.0f;
       scale = n > 0 && full > 0 ? up * coeff / ((float)full * (float)n) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < V * 4; ++i) f[i] = (float)c[i] * unit;
+      for (int i = 0; i < V * 2; ++i) f[i] = pack_f32x2((float)c[2 * i] * unit, (float)c[2 * i + 1] * unit);
     }
   };
-  for (int base = (int)w0; base < r1; base += G * UR) {
-    float v[UR][V * 4];
-    bool live[UR];
+  // the next rows load while these are worked on
+  RowWords<T, V> w[2][UR];
+  bool live[2][UR];
+  auto load = [&](auto buf, int base) {
+    constexpr int B = decltype(buf)::value;
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
-      const int t = base + u * G + g;
-      live[u] = t < r1;
-      const uint8_t m = live[u] && b.mask ? __ldg(b.mask + t) : 1;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        load4<T, VEC>(logits, (long long)t * b.stride, (i * L + l) * 4, b.E, live[u], v[u] + 4 * i);
-      live[u] = live[u] && m;
+      const int t = base + u * G + g, at = min(t, r1 - 1);
+      const uint8_t m = b.mask ? __ldg(b.mask + at) : 1;
+      load_row<T, VEC, V>(static_cast<const uint8_t*>(logits) + (size_t)at * (size_t)b.stride * T::size, l, L, b.E,
+                          w[B][u]);
+      live[B][u] = t < r1 && m;
     }
+  };
+  auto work = [&](auto buf, int base) {
+    constexpr int B = decltype(buf)::value;
 #pragma unroll
     for (int u = 0; u < UR; ++u) {
       const int t = base + u * G + g;
-      if (live[u] && !(t >= s0 && t < s1)) enter(t);
-      const bool in_seq = live[u] && t >= s0 && t < s1;
+      if (live[B][u] && !(t >= s0 && t < s1)) enter(t);
+      const bool in_seq = live[B][u] && t >= s0 && t < s1;
       __syncwarp();
-      float d[V * 4];
-      row_scores<V * 4, SCORE, true>(v[u], d, L);
-      float z = 0.0f, dot = 0.0f;
+      uint64_t v[V * 2], d[V * 2];
+      row_values<T, V>(w[B][u], l, L, b.E, v);
+      row_scores<V * 2, SCORE, true>(v, d, L);
+      uint64_t z2 = v[0], dot2 = mul_f32x2(f[0], v[0]);
 #pragma unroll
-      for (int i = 0; i < V * 4; ++i) {
-        z += v[u][i];
-        dot = __fmaf_rn(f[i], v[u][i], dot);
+      for (int i = 1; i < V * 2; ++i) {
+        z2 = add_f32x2(z2, v[i]);
+        dot2 = fma_f32x2(f[i], v[i], dot2);
       }
-      for (int o = L >> 1; o > 0; o >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      }
-      const float inv = share_factor(z);
-      dot *= inv;
-      const float by = scale * inv;
+      const float inv = share_factor(group_sum(lo_f32(z2) + hi_f32(z2), L));
+      const uint64_t dot = twice(-inv * group_sum(lo_f32(dot2) + hi_f32(dot2), L)), by = twice(scale * inv);
       if (t < r1) {
+        uint8_t* out = static_cast<uint8_t*>(dlogits) + (size_t)t * (size_t)grad_stride * T::size;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int e = (i * L + l) * 4;
           if (e >= b.E) continue;
-          float o[4];
+          uint64_t o[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = in_seq ? by * v[u][4 * i + j] * (f[4 * i + j] - dot) * d[4 * i + j] : 0.0f;
-          const long long at = (long long)t * grad_stride + e;
+          for (int j = 0; j < 2; ++j) {
+            o[j] = mul_f32x2(mul_f32x2(by, v[2 * i + j]), add_f32x2(f[2 * i + j], dot));
+            if (SCORE != MOE_BALANCE_SOFTMAX) o[j] = mul_f32x2(o[j], d[2 * i + j]);
+            o[j] = in_seq ? o[j] : 0;
+          }
           if constexpr (VEC) {
             if constexpr (T::size == 4)
-              *reinterpret_cast<float4*>(static_cast<float*>(dlogits) + at) = make_float4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<ulonglong2*>(out + e * 4) = make_ulonglong2(o[0], o[1]);
             else
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dlogits) + at) =
-                  make_uint2(T::pack(o[0], o[1]), T::pack(o[2], o[3]));
+              *reinterpret_cast<uint2*>(out + e * 2) =
+                  make_uint2(T::pack(lo_f32(o[0]), hi_f32(o[0])), T::pack(lo_f32(o[1]), hi_f32(o[1])));
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (e + j < b.E) {
-                if constexpr (T::size == 4) static_cast<float*>(dlogits)[at + j] = o[j];
-                else static_cast<uint16_t*>(dlogits)[at + j] = T::one(o[j]);
+                const float x = j & 1 ? hi_f32(o[j >> 1]) : lo_f32(o[j >> 1]);
+                if constexpr (T::size == 4) reinterpret_cast<float*>(out)[e + j] = x;
+                else reinterpret_cast<uint16_t*>(out)[e + j] = T::one(x);
               }
           }
         }
       }
+    }
+  };
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  const int step = G * UR;
+  int base = (int)w0;
+  if constexpr (T::size == 2 || V <= 4) {
+    load(B0{}, base);
+#pragma unroll 1
+    for (; base < r1; base += 2 * step) {
+      if (base + step < r1) load(B1{}, base + step);
+      work(B0{}, base);
+      if (base + step >= r1) break;
+      if (base + 2 * step < r1) load(B0{}, base + 2 * step);
+      work(B1{}, base + step);
+    }
+  } else {
+#pragma unroll 1
+    for (; base < r1; base += step) {
+      load(B0{}, base);
+      work(B0{}, base);
     }
   }
 }
@@ -500,6 +638,10 @@ static inline int balance_chunk(int T, int E) {
 // and 9.5.  It walks its sequences one after the other, hence at most 64.
 static inline bool balance_one_block(int T, int E, int S) { return (long long)T * E <= kBalOneBlock && S <= 64; }
 
+// Experts per block of the finish: few where that leaves few blocks, as all of
+// them meet at one counter.
+static inline int balance_finish_experts(int E, int S) { return (long long)S * ((E + 7) / 8) <= 128 ? 8 : 32; }
+
 struct BalanceScratch {
   uint32_t* status;
   BalancePieces pieces;
@@ -514,7 +656,7 @@ static BalanceScratch carve_balance(Carver& c, int T, int E, int S) {
   w.pieces.probs = c.take<float>(pieces * E);
   w.pieces.counts = c.take<int32_t>(pieces * E);
   w.pieces.tokens = c.take<int32_t>(pieces);
-  w.dots = c.take<double>((size_t)S * ((E + 31) / 32));
+  w.dots = c.take<double>((size_t)S * ((E + balance_finish_experts(E, S) - 1) / balance_finish_experts(E, S)));
   return w;
 }
 
@@ -558,8 +700,8 @@ static nvfp4_status with_balance(int dtype, bool vec, int E, int score, F&& f) {
   if (dtype == MXFP4_DTYPE_F16) return by_vec(F16{});
   return by_vec(F32{});
 }
-// Rows in flight per group of lanes.
-constexpr int balance_rows(int v) { return v <= 1 ? 4 : v <= 4 ? 2 : 1; }
+// Rows that a group of lanes takes at once (as many again are being loaded).
+constexpr int balance_rows(int v) { return v <= 1 ? 2 : 1; }
 // Whether rows may be read or written four elements at a time.
 static inline bool balance_vec(const void* p, long long stride, int T, int E, int elem) {
   return E % 4 == 0 && row_access_bytes(p, T > 1 ? stride * elem : 0, elem) >= 4 * elem;
@@ -612,8 +754,10 @@ extern "C" nvfp4_status moe_balance_loss(const void* logits, int dtype, int T, i
                               w.pieces, res);
                         }));
   if (one) return NVFP4_OK;
-  return launch_dependent("balance_finish_kernel", balance_finish_kernel, dim3((unsigned)S, (unsigned)((E + 31) / 32)),
-                          dim3(kFinThreads), 0, s, b, chunk, w.pieces, w.dots, res);
+  const int fe = balance_finish_experts(E, S);
+  return launch_dependent("balance_finish_kernel", fe == 8 ? balance_finish_kernel<8> : balance_finish_kernel<32>,
+                          dim3((unsigned)S, (unsigned)((E + fe - 1) / fe)), dim3(kFinThreads), 0, s, b, chunk, w.pieces,
+                          w.dots, res);
 }
 
 extern "C" nvfp4_status moe_balance_loss_backward(const void* logits, int dtype, int T, int E, long long row_stride,
@@ -638,18 +782,19 @@ extern "C" nvfp4_status moe_balance_loss_backward(const void* logits, int dtype,
   const BalanceShape b{T, E, S, k, balance_lanes(E), row_stride, seq_offsets, token_mask};
   const int elem = mx_elem_size(dtype);
   const bool vec = balance_vec(logits, row_stride, T, E, elem) && balance_vec(dlogits, grad_stride, T, E, elem);
-  // about three blocks an SM (what fits at once); a warp takes neighbouring
-  // rows, so that it seldom changes sequence
-  const int per_iter = 32 / b.lanes;
-  const long long warps = (long long)sms * 3 * kBalWarps;
-  const int rows_per_warp = (int)(((T + warps - 1) / warps + per_iter - 1) / per_iter) * per_iter;
-  const long long rows_per_block = (long long)rows_per_warp * kBalWarps;
-  const dim3 grid((unsigned)((T + rows_per_block - 1) / rows_per_block));
   return with_balance(dtype, vec, E, score, [&](auto tag, auto vv, auto v, auto sc) -> nvfp4_status {
+    using TT = decltype(tag);
     constexpr int V = decltype(v)::value;
+    // what fits an SM at once; a warp takes neighbouring rows, so that it
+    // seldom changes sequence
+    const int per_iter = 32 / b.lanes;
+    const long long warps = (long long)sms * balance_backward_blocks(V, TT::size) * kBalWarps;
+    const int rows_per_warp = (int)(((T + warps - 1) / warps + per_iter - 1) / per_iter) * per_iter;
+    const long long rows_per_block = (long long)rows_per_warp * kBalWarps;
+    const dim3 grid((unsigned)((T + rows_per_block - 1) / rows_per_block));
     return launch_dependent(
         "balance_backward_kernel",
-        balance_backward_kernel<decltype(tag), decltype(vv)::value, V, balance_rows(V), decltype(sc)::value>, grid,
+        balance_backward_kernel<TT, decltype(vv)::value, V, balance_rows(V), decltype(sc)::value>, grid,
         dim3(kBalThreads), 0, as_stream(stream), logits, b, rows_per_warp, coeff, counts, tokens, grad_loss, dlogits,
         grad_stride);
   });

@@ -32,7 +32,7 @@
 //   8192 x 4096 x 6144   72 us, 5.7 PFLOP/s (0.86 of four times the measured
 //                        bf16 rate)
 //   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 8.6
-//   16 x 6144 x 6144     6.8 us, 2.9 TB/s; 1 x 6144 x 6144 6.5 us
+//   16 x 6144 x 6144     8.1 us, 2.4 TB/s; 1 x 6144 x 6144 7.5 us (b in L2: 6.8, 6.5)
 //   1 x 6144 x 6144 with x quantised in the same kernel 7.9 us (two kernels 9.5)
 //   16 tokens, top-8 of 80 experts, 4096 x 6144: 140 us, 97 % of the copy rate
 // What brought it there, at 8192 x 4096 x 6144: one CTA a tile, the accumulator
