@@ -633,10 +633,11 @@ static inline int balance_chunk(int T, int E) {
   return std::max(1, (int)(((long long)T + 148ll * 3 * step - 1) / (148ll * 3 * step))) * step;
 }
 // Few logits: one block does the whole forward, one launch instead of two.
-// Measured, one block against two kernels (us): 16 x 80 3.7 and 8.8, 64 x 80
-// 4.1 and 8.9, 128 x 128 6.3 and 9.5, 256 x 128 9.4 and 9.6, 512 x 128 15.5
-// and 9.5.  It walks its sequences one after the other, hence at most 64.
-static inline bool balance_one_block(int T, int E, int S) { return (long long)T * E <= kBalOneBlock && S <= 64; }
+// Measured, one block against two kernels (us): 16 x 80 3.5 and 7.8, 64 x 80
+// 4.3 and 7.9, 128 x 128 6.2 and 8.5, 192 x 128 7.7 and 8.4, 256 x 128 9.1 and
+// 8.4, 512 x 128 14.7 and 8.1.  It walks its sequences one after the other, 2.3
+// us each (128 x 128 in 20: 50 and 27, in 60: 144 and 47), hence at most two.
+static inline bool balance_one_block(int T, int E, int S) { return (long long)T * E <= kBalOneBlock && S <= 2; }
 
 // Experts per block of the finish: few where that leaves few blocks, as all of
 // them meet at one counter.
