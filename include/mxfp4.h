@@ -84,8 +84,9 @@ NVFP4_API nvfp4_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* sca
  * [expert_offsets[e], expert_offsets[e] + expert_counts[e]) of a meet expert
  * e's matrix; expert_counts NULL means the whole segment.  Offsets are
  * non-decreasing multiples of 128 as moe_route writes them; values outside
- * [0, M] are clamped.  Rows of y that belong to no expert keep what they
- * held.  Dense: E = 0 and expert_offsets = expert_counts = NULL; every row is
+ * [0, M] are clamped (M may be any number: the last segment may end inside its
+ * padding), and a segment that then starts elsewhere than at a multiple of 128
+ * has no rows.  Rows of y that belong to no expert keep what they held.  Dense: E = 0 and expert_offsets = expert_counts = NULL; every row is
  * written.
  *
  * a codes, b codes and scales need 16-byte alignment.  E <= 1024, M, N and K

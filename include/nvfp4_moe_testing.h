@@ -101,6 +101,13 @@ NVFP4_API int nvfp4_test_router_splits(int T, int H, int* stages_per_split);
  * for sizes that mxfp4_matmul refuses. */
 NVFP4_API int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages);
 
+/* Host arithmetic only: the rows [row0[e], row0[e] + rows[e]) that expert e's
+ * matrix meets in a grouped product of M rows, from `offsets` [E + 1] and
+ * `counts` [E] (nullable), all in host memory.  Returns -1 for a NULL pointer
+ * or sizes that mxfp4_matmul refuses. */
+NVFP4_API int nvfp4_test_mxfp4_segments(const int32_t* offsets, const int32_t* counts, int M, int E, int* row0,
+                                        int* rows);
+
 /* Host arithmetic only: whether a dense mxfp4_linear of M rows of `dtype`
  * quantises them inside the product (on 148 SMs, y apart from x); `wide`: the
  * rows of x are 16-byte aligned.  Then *stages (nullable) gets the pipeline

@@ -125,6 +125,7 @@ _declare("nvfp4_test_block_scale_div", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp
 _declare("nvfp4_test_router_splits", _i, _i, _i, ctypes.POINTER(ctypes.c_int))
 _declare("nvfp4_test_mxfp4_plan", _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
          ctypes.POINTER(ctypes.c_int))
+_declare("nvfp4_test_mxfp4_segments", _i, _vp, _vp, _i, _i, _vp, _vp)
 _declare("nvfp4_test_mxfp4_fuses", _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int))
 
 # Every symbol the public headers declare (checked by the CPU test suite).
@@ -143,7 +144,8 @@ EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
            "nvfp4_test_e2m1", "nvfp4_test_e2m1_sweep", "nvfp4_test_e4m3", "nvfp4_test_sigmoid",
            "nvfp4_test_mma_peak", "nvfp4_test_wait_timeout", "nvfp4_test_block_scale_div",
-           "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan", "nvfp4_test_mxfp4_fuses")
+           "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan", "nvfp4_test_mxfp4_segments",
+           "nvfp4_test_mxfp4_fuses")
 
 
 def _check(status: int):
@@ -1016,6 +1018,18 @@ def nvfp4_test_mxfp4_plan(M: int, N: int, K: int, E: int = 0):
     if nt < 0:
         raise ValueError(f"no MXFP4 product has M={M} N={N} K={K} E={E}")
     return nt, v[0].value, bool(v[1].value), v[2].value
+
+
+def nvfp4_test_mxfp4_segments(offsets, counts, M: int):
+    """[(first row, rows)] of each expert in a grouped product of M rows, from
+    lists of E + 1 offsets and E counts (or None)."""
+    E = len(offsets) - 1
+    ints = ctypes.c_int32 * E
+    row0, rows = ints(), ints()
+    if lib.nvfp4_test_mxfp4_segments((ctypes.c_int32 * (E + 1))(*offsets), ints(*counts) if counts else None, M, E,
+                                     row0, rows) < 0:
+        raise ValueError(f"no MXFP4 product has M={M} and {E} experts")
+    return list(zip(row0, rows))
 
 
 def nvfp4_test_mxfp4_fuses(M: int, N: int, K: int, dtype: torch.dtype, wide: bool = True):

@@ -3,6 +3,8 @@
 // quantisers and the products.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "host.cuh"
 #include "../../include/mxfp4.h"
@@ -19,6 +21,21 @@ __host__ __device__ inline int mx_row_bytes(int cols) { return mx_blocks(cols) *
 // Byte offset of the four scales of (row, block group) in the tiled layout.
 NVDEV size_t mx_tiled_offset(int row, int group, int groups) {
   return ((size_t)(row >> 7) * groups + group) * kAtomBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// The rows that expert e's matrix meets in a product of M rows.  Offsets and
+// counts come from the device and are not trusted: a segment is clamped to
+// [0, M] and its rows to the segment, so one that starts at or past M is empty
+// whatever M is.  Scale tiles hold 128 rows: a segment that starts inside one
+// has no rows.
+struct MxSegment {
+  int row0, rows;
+};
+__host__ __device__ inline MxSegment mx_segment(const int32_t* offsets, const int32_t* counts, int M, int e) {
+  const int lo = std::min(std::max(offsets[e], 0), M), hi = std::min(std::max(offsets[e + 1], lo), M);
+  int n = lo % 128 ? 0 : hi - lo;
+  if (counts) n = std::min(n, std::max(counts[e], 0));
+  return {lo, n};
 }
 
 // Element types of unquantised matrices (MXFP4_DTYPE_*), as tags.

@@ -134,9 +134,7 @@ struct MxTile {
 };
 
 // Grouped products: every expert's first tile group (`nt` tokens of one
-// expert), first row and tokens, in shared memory behind the stages.  The
-// device-side offsets are not trusted: a segment is clamped to [0, M] and its
-// tokens to the segment.
+// expert), first row and tokens, in shared memory behind the stages.
 struct MxSegments {
   int *start, *row0, *tokens;      // [E + 1], [E], [E]
 };
@@ -154,14 +152,10 @@ NVDEV MxSegments mx_scan_segments(const MxGemmParams& p, uint8_t* at) {
       const int e = e0 + lane;
       int v = 0;
       if (e < p.E) {
-        const int lo = min(max(p.expert_offsets[e], 0), p.M);
-        const int hi = min(max(p.expert_offsets[e + 1], lo), p.M);
-        const int r = lo & ~127;                 // a multiple of 128 by contract; never past the scale tiles
-        int n = hi - r;
-        if (p.expert_counts) n = min(n, max(p.expert_counts[e], 0));
-        g.row0[e] = r;
-        g.tokens[e] = n;
-        v = (n + p.nt - 1) / p.nt;
+        const MxSegment s = mx_segment(p.expert_offsets, p.expert_counts, p.M, e);
+        g.row0[e] = s.row0;
+        g.tokens[e] = s.rows;
+        v = (s.rows + p.nt - 1) / p.nt;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1416,4 +1410,15 @@ extern "C" int nvfp4_test_mxfp4_fuses(int M, int N, int K, int dtype, int wide, 
   if (stages) *stages = pl.stages;
   if (ctas_per_sm) *ctas_per_sm = pl.ctas_per_sm;
   return 1;
+}
+
+extern "C" int nvfp4_test_mxfp4_segments(const int32_t* offsets, const int32_t* counts, int M, int E, int* row0,
+                                         int* rows) {
+  if (!offsets || !row0 || !rows || M < 0 || E < 1 || E > kXMaxE) return -1;
+  for (int e = 0; e < E; ++e) {
+    const MxSegment s = mx_segment(offsets, counts, M, e);
+    row0[e] = s.row0;
+    rows[e] = s.rows;
+  }
+  return 0;
 }

@@ -339,6 +339,37 @@ def test_grouped_offsets_outside_the_rows_are_clamped():
     assert (np.abs(y - ref) <= 66 * 2.0 ** -23 * 64 * 36 * np.abs(av).max() * np.abs(bv).max()).all()
 
 
+@pytest.mark.parametrize("M,offsets,N,K,dtype", [
+    (300, [0, 384, 384], 128, 64, torch.float32),
+    (300, [0, 128, 384, 384, 512], 256, 288, torch.bfloat16),
+    (1, [0, 128, 128, 256], 128, 96, torch.float16),
+    (3400, [0, 1152, 3456, 3456, 3584], 2048, 1700, torch.bfloat16),      # on CTA pairs
+])
+def test_grouped_rows_that_end_inside_the_last_segment(M, offsets, N, K, dtype):
+    """A last segment whose padding was trimmed, with empty experts behind it:
+    they have no rows, with and without counts."""
+    require_cuda()
+    c = capi()
+    E = len(offsets) - 1
+    assert c.nvfp4_test_mxfp4_plan(M, N, K, E)[2] == (M == 3400)
+    a, av = operand(M, K, 1)
+    b, bv = operand(E * N, K, 2)
+    lim = np.clip(offsets, 0, M)
+    ref = np.zeros((M, N))
+    bound = np.zeros((M, N))
+    for e in range(E):
+        r = slice(lim[e], lim[e + 1])
+        ref[r] = av[r] @ bv[e * N:(e + 1) * N].T
+        bound[r] = product_bound(av[r], bv[e * N:(e + 1) * N], ref[r], dtype)
+    fine = np.abs(ref) < torch.finfo(dtype).max / 2
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    counts = torch.from_numpy(np.diff(lim).astype(np.int32)).cuda()
+    counts[-1] = 5                                          # of a segment past the rows
+    for cnt in (None, counts):
+        y = c.mxfp4_matmul(a, b, out_dtype=dtype, expert_offsets=off, expert_counts=cnt)
+        assert (np.abs(np64(y) - ref) <= bound)[fine].all()
+
+
 def test_linear_is_quantize_then_matmul():
     require_cuda()
     c = capi()

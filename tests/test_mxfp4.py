@@ -196,6 +196,39 @@ def test_product_plans():
             plan(*bad)
 
 
+def test_segments_of_grouped_products():
+    """Host arithmetic shared with the kernels: whatever the number of rows,
+    each expert has the clamped rows of its own segment and no others."""
+    seg = capi().nvfp4_test_mxfp4_segments
+    rows = lambda s: [(a, n) for a, n in s if n]  # noqa: E731
+    # segments that start at or past the rows' end are empty: no 128-row tile is taken twice
+    assert rows(seg([0, 384, 384], None, 300)) == [(0, 300)]
+    assert rows(seg([0, 384, 384], [300, 0], 300)) == [(0, 300)]
+    assert rows(seg([0, 384, 512, 512], [300, 77, 9], 300)) == [(0, 300)]
+    assert rows(seg([0, 128, 256, 384, 640], None, 257)) == [(0, 128), (128, 128), (256, 1)]
+    assert rows(seg([-128, 128, 1 << 30, 0], [1 << 30, 1 << 30, -5], 256)) == [(0, 128), (128, 128)]
+    assert rows(seg([-2 ** 31, 2 ** 31 - 1], None, 1)) == [(0, 1)] and rows(seg([0, 128], None, 0)) == []
+    assert rows(seg([0, 100, 256], None, 256)) == [(0, 100)]           # a start inside a scale tile
+    rng = np.random.default_rng(0)
+    for _ in range(2000):
+        E, M = int(rng.integers(1, 12)), int(rng.integers(0, 1500))
+        off = np.concatenate([[rng.integers(-2, 2)], rng.integers(0, 4, E)]).cumsum() * 128
+        cnt = [int(v) for v in rng.integers(-10, 500, E)] if rng.random() < 0.5 else None
+        owner = np.full(M, -1)
+        for e, (a, n) in enumerate(seg([int(v) for v in off], cnt, M)):
+            assert n >= 0 and (n == 0 or (a % 128 == 0 and 0 <= a and a + n <= M))
+            assert (owner[a:a + n] == -1).all()
+            owner[a:a + n] = e
+        lim = np.clip(off, 0, M)
+        want = np.full(M, -1)
+        for e in range(E):
+            n = lim[e + 1] - lim[e] if cnt is None else min(lim[e + 1] - lim[e], max(cnt[e], 0))
+            want[lim[e]:lim[e] + n] = e
+        assert np.array_equal(owner, want)
+    with pytest.raises(ValueError):
+        seg([0, 128], None, -1)
+
+
 def test_products_that_quantise_their_rows():
     """Host arithmetic: shared memory and tiles of a fused mxfp4_linear fit."""
     c = capi()
