@@ -177,10 +177,10 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const uint8_t* 
 }
 
 // The gathered rows of a grouped product, one block a row.  Rows without a
-// source are zeros where a product reads them, inside an expert's tokens (row
-// r of expert e for offsets[e] <= r < offsets[e] + counts[e]); outside, where
-// most of a decoding step's rows lie (127 of padding an expert), nothing is
-// written.
+// source are zeros where a product reads them, inside an expert's tokens (the
+// product's own mx_segment of the last expert that starts at or before the
+// row); outside, where most of a decoding step's rows lie (127 of padding an
+// expert), nothing is written.
 constexpr int kMxRowThreads = 128;
 constexpr int kMxRowUnits = 3;
 template <typename T, int VB>
@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kMxRowThreads) mx_quantize_rows_kernel(
       const int e = e0 + (int)threadIdx.x;
       before += __syncthreads_count(e < E && __ldg(offsets + e) <= row);
     }
-    if (before == 0 || row - __ldg(offsets + before - 1) >= __ldg(counts + before - 1)) return;
+    if (before == 0) return;
+    const MxSegment seg = mx_segment(offsets, counts, (int)gridDim.x, before - 1);
+    if (row - seg.row0 >= seg.rows) return;
   }
   const int n = live ? cols : 0, groups = mx_groups(cols);
   const int sub = threadIdx.x / LPU, l = threadIdx.x & (LPU - 1);

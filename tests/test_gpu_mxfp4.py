@@ -492,6 +492,30 @@ def test_grouped_linear_with_padding_rows(with_counts):
         assert torch.equal(out[r], (rw[r] * bias[e * N:(e + 1) * N]).to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("offsets,counts", [([-128, 128, 256], [100, 7]), ([-384, -128, 1 << 30], [50, 200]),
+                                            ([-2 ** 31, 256, 2 ** 31 - 1], [2 ** 31 - 1, 9])])
+def test_grouped_linear_with_clamped_offsets(offsets, counts):
+    """Rows without a source are zeros wherever the product reads them, which
+    for an offset outside the rows is counted from its clamped value."""
+    require_cuda()
+    c = capi()
+    E, N, K, M = 2, 128, 200, 256
+    x = matrix(60, K, torch.bfloat16, special=False).cuda()
+    w, _ = operand(E * N, K, 4)
+    bias = torch.randn(E * N, device="cuda")
+    perm = torch.arange(M, dtype=torch.int32) % 60
+    perm[::3] = -1
+    perm = perm.cuda()
+    kw = dict(bias=bias, expert_offsets=torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+              expert_counts=torch.tensor(counts, dtype=torch.int32, device="cuda"))
+    ws = torch.full((c.mxfp4_linear_workspace_size(M, K),), 255, dtype=torch.uint8, device="cuda")   # NaN scales
+    out = torch.full((M, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    c.mxfp4_linear(x, w, perm=perm, out=out, workspace=ws, **kw)
+    want = torch.full_like(out, 9.0)
+    c.mxfp4_matmul(c.mxfp4_quantize(x, perm=perm), w, out=want, **kw)
+    assert torch.isfinite(out).all() and torch.equal(out, want)
+
+
 def test_results_do_not_change_from_run_to_run():
     require_cuda()
     c = capi()
