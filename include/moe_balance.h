@@ -50,8 +50,9 @@ NVFP4_API nvfp4_status moe_balance_loss(const void* logits, int dtype, int T, in
 
 /* dlogits[T][E] (the logits' dtype, rows grad_stride elements apart) =
  * grad_loss[0] * dloss/dlogits from the counts and tokens of the forward call
- * with the same arguments.  Every element is written.  dlogits may not be
- * logits itself. */
+ * with the same arguments.  Every element is written.  dlogits may not share
+ * elements with logits: where their memory meets, they are different columns
+ * of one buffer, with one stride. */
 NVFP4_API nvfp4_status moe_balance_loss_backward(const void* logits, int dtype, int T, int E, long long row_stride,
                                                  int k, int score, const uint8_t* token_mask,
                                                  const int32_t* seq_offsets, int S, float coeff,

@@ -708,6 +708,20 @@ static inline bool balance_vec(const void* p, long long stride, int T, int E, in
   return E % 4 == 0 && row_access_bytes(p, T > 1 ? stride * elem : 0, elem) >= 4 * elem;
 }
 
+// Whether the gradient may share elements with the logits, whose rows are
+// loaded ahead of the stores.  Matrices whose memory meets are apart when they
+// are different columns of one buffer: equal strides, and the one's row between
+// the other's row and the next.
+static bool shares_elements(const void* logits, long long stride, const void* dlogits, long long grad_stride, int T,
+                            int E, int elem) {
+  if (!overlap(logits, T, stride, E, elem, dlogits, T, grad_stride, E, elem)) return false;
+  if (T <= 1 || stride != grad_stride) return true;
+  const long long pitch = stride * elem, width = (long long)E * elem;
+  const long long by = (long long)(reinterpret_cast<intptr_t>(dlogits) - reinterpret_cast<intptr_t>(logits));
+  const long long column = (by % pitch + pitch) % pitch;
+  return column < width || column + width > pitch;
+}
+
 }  // namespace nvfp4moe
 
 using namespace nvfp4moe;
@@ -771,17 +785,17 @@ extern "C" nvfp4_status moe_balance_loss_backward(const void* logits, int dtype,
   if (T == 0) return NVFP4_OK;
   NV_REQUIRE(counts && tokens && grad_loss && dlogits, NVFP4_ERR_INVALID_ARG,
              "moe_balance_loss_backward: a required pointer is NULL");
-  NV_REQUIRE(dlogits != logits, NVFP4_ERR_INVALID_ARG,
-             "moe_balance_loss_backward: dlogits may not take the place of logits");
   NV_REQUIRE(T <= 1 || grad_stride >= E, NVFP4_ERR_INVALID_ARG,
              "moe_balance_loss_backward: gradient stride %lld is below E=%d", grad_stride, E);
-  NV_REQUIRE(aligned(dlogits, mx_elem_size(dtype)) && aligned(counts, 4) && aligned(tokens, 4) &&
+  const int elem = mx_elem_size(dtype);
+  NV_REQUIRE(!shares_elements(logits, row_stride, dlogits, grad_stride, T, E, elem), NVFP4_ERR_INVALID_ARG,
+             "moe_balance_loss_backward: dlogits may not take the place of logits, whole or in part");
+  NV_REQUIRE(aligned(dlogits, elem) && aligned(counts, 4) && aligned(tokens, 4) &&
                  aligned(grad_loss, 4),
              NVFP4_ERR_INVALID_ARG, "moe_balance_loss_backward: a tensor is not aligned to its elements");
   int sms = 0;
   NV_CHECK(device_sm_count(&sms));
   const BalanceShape b{T, E, S, k, balance_lanes(E), row_stride, seq_offsets, token_mask};
-  const int elem = mx_elem_size(dtype);
   const bool vec = balance_vec(logits, row_stride, T, E, elem) && balance_vec(dlogits, grad_stride, T, E, elem);
   return with_balance(dtype, vec, E, score, [&](auto tag, auto vv, auto v, auto sc) -> nvfp4_status {
     using TT = decltype(tag);

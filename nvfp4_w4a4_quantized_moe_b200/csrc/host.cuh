@@ -46,6 +46,15 @@ struct Carver {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether the memory from the first to the last element of two matrices meets.
+inline bool overlap(const void* a, int a_rows, long long a_stride, int a_cols, int a_elem, const void* b, int b_rows,
+                    long long b_stride, int b_cols, int b_elem) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t a1 = a0 + ((uintptr_t)(a_rows > 1 ? (a_rows - 1) * a_stride : 0) + (uintptr_t)a_cols) * a_elem;
+  const uintptr_t b1 = b0 + ((uintptr_t)(b_rows > 1 ? (b_rows - 1) * b_stride : 0) + (uintptr_t)b_cols) * b_elem;
+  return a0 < b1 && b0 < a1;
+}
+
 // Launches `kernel` as a programmatic dependent of the stream's previous
 // kernel: its blocks may start once every block of that kernel has signalled
 // (griddepcontrol.launch_dependents), and the kernel itself waits for the

@@ -1317,15 +1317,6 @@ extern "C" nvfp4_status mxfp4_matmul(const uint8_t* a_codes, const uint8_t* a_sc
   return launch_mx_gemm(g, plan_mx_gemm(M, N, K, E, sms), sms, as_stream(stream));
 }
 
-// Whether the memory from the first to the last element of two matrices meets.
-static bool overlap(const void* a, int a_rows, long long a_stride, int a_cols, int a_elem, const void* b, int b_rows,
-                    long long b_stride, int b_cols, int b_elem) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  const uintptr_t a1 = a0 + ((uintptr_t)(a_rows > 1 ? (a_rows - 1) * a_stride : 0) + (uintptr_t)a_cols) * a_elem;
-  const uintptr_t b1 = b0 + ((uintptr_t)(b_rows > 1 ? (b_rows - 1) * b_stride : 0) + (uintptr_t)b_cols) * b_elem;
-  return a0 < b1 && b0 < a1;
-}
-
 struct MxLinearScratch {
   uint32_t* status;
   uint8_t *codes, *scales;

@@ -257,3 +257,26 @@ def test_binding_refusals():
             call()
     with pytest.raises(c.Nvfp4Error):
         c.moe_balance_loss(l, idx, 0.1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_beside_and_over_the_logits(dtype):
+    """Logits and gradient as two column ranges of one buffer give what they
+    give apart; a gradient that shares elements with the logits is refused and
+    leaves them as they were."""
+    require_cuda()
+    c = capi()
+    T, E = 3000, 24
+    logits, idx = inputs(T, E, 3, DTYPES[dtype])
+    one = torch.ones(1, device="cuda")
+    both = torch.zeros(T + 1, 2 * E, dtype=DTYPES[dtype], device="cuda")
+    both[:T, :E] = logits.cuda()
+    r = c.moe_balance_loss(both[:T, :E], idx.cuda(), 64.0)
+    want = c.moe_balance_loss_backward(logits.cuda(), r, one)
+    before = both.clone()
+    for out in (both[:T, :E], both[1:, :E], both[:T, E - 4:2 * E - 4], both[:T, 4:E + 4]):
+        with pytest.raises(c.Nvfp4Error, match="place"):
+            c.moe_balance_loss_backward(both[:T, :E], r, one, out=out)
+    assert torch.equal(both, before)
+    c.moe_balance_loss_backward(both[:T, :E], r, one, out=both[:T, E:])
+    assert torch.equal(both[:T, E:], want) and torch.equal(both[:T, :E], before[:T, :E])

@@ -279,6 +279,35 @@ def test_balance_refusals():
     assert c.moe_balance_loss_workspace_size(0, 8) > 0 and c.moe_balance_loss_workspace_size(4, 0) == 0
 
 
+def test_balance_gradient_over_part_of_the_logits_is_refused():
+    """Logits of 4 x 8 fp32, rows `st` elements apart, at 0x10000.  A call that
+    is not refused for its memory is refused for the misaligned grad_loss
+    behind it, so nothing is launched."""
+    lib = capi().lib
+    base = 0x10000
+
+    def refused(by, st=8, gs=None, T=4, dt=2, E=8):
+        r = lib.moe_balance_loss_backward(ctypes.c_void_p(base), dt, T, E, st, 2, 0, None, None, 1, 0.1, FAKE, FAKE,
+                                          ctypes.c_void_p(0x1001), ctypes.c_void_p(base + by), gs or st, None)
+        assert r == 1
+        return b"place" in lib.nvfp4_last_error()
+    assert refused(0) and refused(0, T=1) and refused(0, st=20)
+    for rows in (1, 2, 3, -1, -3):                       # shifted by rows
+        assert refused(32 * rows) and refused(80 * rows, st=20)
+    assert not refused(128) and not refused(-128) and not refused(32, T=1) and refused(28, T=1)
+    assert refused(4) and refused(-4) and refused(124) and refused(-124)
+    # other columns of one buffer: apart while the rows do not meet
+    assert not refused(32, st=20) and not refused(48, st=20) and refused(28, st=20) and refused(52, st=20)
+    assert not refused(32, st=16) and not refused(-32, st=16) and refused(36, st=16)
+    assert not refused(80 + 40, st=20) and not refused(-80 + 40, st=20) and refused(-80 + 52, st=20)
+    # other strides over the same memory are refused, over other memory not
+    assert refused(32, st=20, gs=24) and refused(0, st=16, gs=8) and not refused(320, st=20, gs=8)
+    # two-byte elements; T and strides whose extent passes 32 bits
+    assert refused(16, dt=0) and not refused(64, dt=0) and not refused(16, st=16, dt=0)
+    big = 1 << 20
+    assert refused(4 * big * 4095, st=big, T=4096) and not refused(4 * big * 4095 + 32, st=big, T=4096)
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     c = capi()
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
