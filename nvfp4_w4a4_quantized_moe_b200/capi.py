@@ -650,6 +650,16 @@ def _same_device(dev: int, *tensors):
             raise ValueError(f"all tensors of a call must be on one device: got {t.device} and cuda:{dev}")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int32(n: int, name: str) -> int:
+    """n, if the library's int holds it (ctypes would pass its low 32 bits)."""
+    if n > _INT_MAX:
+        raise ValueError(f"{name} is {n}; the library takes sizes below 2^31")
+    return n
+
+
 def _matrix(t, name: str, dtypes=_DTYPES):
     """(rows, cols, row stride) of a CUDA matrix whose rows are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -660,6 +670,8 @@ def _matrix(t, name: str, dtypes=_DTYPES):
     if len(shape) != 2 or shape[1] < 1:
         raise ValueError(f"{name} must be a matrix with at least one column, got shape {tuple(shape)}")
     rows, cols = shape
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise ValueError(f"{name} is {rows} x {cols}; the library takes sizes below 2^31")
     if cols > 1 and strides[1] != 1:
         raise ValueError(f"{name} must have contiguous rows (stride {strides})")
     if rows > 1 and strides[0] < cols:
@@ -704,6 +716,7 @@ class Mxfp4:
         _cuda(self.scales, torch.uint8, "scales")
         if self.rows < 0 or self.cols < 1:
             raise ValueError(f"no MXFP4 matrix has shape {self.rows} x {self.cols}")
+        _int32(max(self.rows, self.cols), "the matrix's larger side")
         row_bytes, scale_bytes = _mx_sizes(self.rows, self.cols, self.layout)
         if self.codes.numel() < self.rows * row_bytes:
             raise ValueError(f"codes hold {self.codes.numel()} bytes; a {self.rows} x {self.cols} matrix has "
@@ -742,7 +755,7 @@ def mxfp4_quantize(x: torch.Tensor, layout: str = "tiled", perm: torch.Tensor | 
             raise ValueError("a stack of matrices must be contiguous")
         x = x.flatten(0, 1)
     rows, cols, stride = _matrix(x, "x")
-    n = rows if perm is None else _cuda(perm, torch.int32, "perm").numel()
+    n = rows if perm is None else _int32(_cuda(perm, torch.int32, "perm").numel(), "perm's length")
     q = _mx_out(out, n, cols, layout, x.device)
     dev = x.get_device()
     _same_device(dev, perm, q.codes)
@@ -789,7 +802,7 @@ def _product_args(M: int, b: Mxfp4, out_dtype, out, bias, row_weight, expert_off
         raise ValueError("a product takes tiled scales; quantise with layout='tiled'")
     E, N = 0, b.rows
     if expert_offsets is not None:
-        E = _cuda(expert_offsets, torch.int32, "expert_offsets").numel() - 1
+        E = _int32(_cuda(expert_offsets, torch.int32, "expert_offsets").numel() - 1, "the number of experts")
         if E < 1 or N % E:
             raise ValueError(f"expert_offsets of {E + 1} entries do not divide b's {N} rows into experts")
         N //= E
@@ -846,7 +859,7 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out_dtype: torch.dtype = torch.bfloat16, ou
 
 
 def mxfp4_linear_workspace_size(M: int, K: int) -> int:
-    return lib.mxfp4_linear_workspace_size(M, K)
+    return lib.mxfp4_linear_workspace_size(_int32(M, "M"), _int32(K, "K"))
 
 
 def mxfp4_linear(x: torch.Tensor, w: Mxfp4, out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
@@ -859,7 +872,7 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4, out_dtype: torch.dtype | None = None
     rows, K, x_stride = _matrix(x, "x")
     if K != w.cols:
         raise ValueError(f"x has {K} columns and w {w.cols}")
-    M = rows if perm is None else _cuda(perm, torch.int32, "perm").numel()
+    M = rows if perm is None else _int32(_cuda(perm, torch.int32, "perm").numel(), "perm's length")
     dtype = x.dtype
     E, N, out, stride = _product_args(M, w, out_dtype or dtype, out, bias, row_weight, expert_offsets, expert_counts)
     if workspace is None:
@@ -898,7 +911,7 @@ class BalanceLoss:
 
 
 def moe_balance_loss_workspace_size(T: int, E: int, S: int = 1) -> int:
-    return lib.moe_balance_loss_workspace_size(T, E, S)
+    return lib.moe_balance_loss_workspace_size(_int32(T, "T"), _int32(E, "E"), _int32(S, "S"))
 
 
 def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float, score: str = "sigmoid",
@@ -913,6 +926,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
     idx_shape = _cuda(topk_idx, torch.int32, "topk_idx").shape
     if len(idx_shape) != 2 or idx_shape[0] != T:
         raise ValueError(f"topk_idx must be [{T}, k], got {tuple(idx_shape)}")
+    k = _int32(idx_shape[1], "k")
     if score not in BALANCE_SCORES:
         raise ValueError(f"score must be one of {', '.join(BALANCE_SCORES)}, got {score!r}")
     if token_mask is not None:
@@ -921,7 +935,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
         _vector(token_mask, torch.uint8, "token_mask", T)
     S = 1
     if seq_offsets is not None:
-        S = _cuda(seq_offsets, torch.int32, "seq_offsets").numel() - 1
+        S = _int32(_cuda(seq_offsets, torch.int32, "seq_offsets").numel() - 1, "the number of sequences")
         if S < 1:
             raise ValueError("seq_offsets must hold at least two values")
     device = logits.device
@@ -936,9 +950,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
     dev = logits.get_device()
     _same_device(dev, topk_idx, token_mask, seq_offsets, workspace)
     _launch(dev, lib.moe_balance_loss, logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, topk_idx.data_ptr(),
-            idx_shape[1], BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff, loss.data_ptr(),
+            k, BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff, loss.data_ptr(),
             counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return BalanceLoss(loss, counts, tokens, probs, idx_shape[1], score, coeff, token_mask, seq_offsets)
+    return BalanceLoss(loss, counts, tokens, probs, k, score, coeff, token_mask, seq_offsets)
 
 
 def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss: torch.Tensor,

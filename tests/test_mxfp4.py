@@ -308,6 +308,43 @@ def test_balance_gradient_over_part_of_the_logits_is_refused():
     assert refused(4 * big * 4095, st=big, T=4096) and not refused(4 * big * 4095 + 32, st=big, T=4096)
 
 
+class ShapeOnly(torch.Tensor):
+    """A tensor without memory that the binding takes for one on the device."""
+    is_cuda = True
+
+    @staticmethod
+    def of(*shape, dtype):
+        return torch.Tensor._make_subclass(ShapeOnly, torch.empty(*shape, dtype=dtype, device="meta"))
+
+
+def test_sizes_past_32_bits_are_refused():
+    """2^32 + 4 rows must not reach the library as 4."""
+    c = capi()
+    n = 2 ** 32 + 4
+    t = ShapeOnly.of
+    small, idx = t(4, 8, dtype=torch.float32), t(4, 2, dtype=torch.int32)
+    long_idx = t(n, dtype=torch.int32)
+    q = c.Mxfp4.__new__(c.Mxfp4)
+    q.codes, q.scales, q.rows, q.cols, q.layout = t(4, 16, dtype=torch.uint8), t(512, dtype=torch.uint8), 4, 8, "tiled"
+    for call in (lambda: c.mxfp4_quantize(t(n, 8, dtype=torch.bfloat16)),
+                 lambda: c.mxfp4_quantize(t(4, n, dtype=torch.bfloat16)),
+                 lambda: c.mxfp4_quantize(t(2 ** 31, 2, 2, dtype=torch.float16)),
+                 lambda: c.mxfp4_quantize(small, perm=long_idx),
+                 lambda: c.mxfp4_quantize_transposed(t(n, 8, dtype=torch.float32)),
+                 lambda: c.mxfp4_dequantize(q, out=t(n, 8, dtype=torch.float32)),
+                 lambda: c.Mxfp4(t(n, 16, dtype=torch.uint8), t(2 ** 40, dtype=torch.uint8), n, 8),
+                 lambda: c.mxfp4_linear(t(n, 8, dtype=torch.float32), q),
+                 lambda: c.mxfp4_linear(small, q, perm=long_idx),
+                 lambda: c.mxfp4_matmul(q, q, expert_offsets=long_idx),
+                 lambda: c.mxfp4_linear_workspace_size(n, 8), lambda: c.mxfp4_linear_workspace_size(8, n),
+                 lambda: c.moe_balance_loss(t(n, 8, dtype=torch.float32), t(n, 2, dtype=torch.int32), 0.1),
+                 lambda: c.moe_balance_loss(small, t(4, n, dtype=torch.int32), 0.1),
+                 lambda: c.moe_balance_loss(small, idx, 0.1, seq_offsets=long_idx),
+                 lambda: c.moe_balance_loss_workspace_size(n, 8), lambda: c.moe_balance_loss_workspace_size(4, 8, n)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     c = capi()
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
