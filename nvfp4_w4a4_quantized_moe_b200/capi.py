@@ -908,6 +908,7 @@ class BalanceLoss:
     coeff: float
     token_mask: torch.Tensor | None
     seq_offsets: torch.Tensor | None
+    n_tokens: int | None = None      # rows of the logits, where the object comes from moe_balance_loss
 
 
 def moe_balance_loss_workspace_size(T: int, E: int, S: int = 1) -> int:
@@ -952,7 +953,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
     _launch(dev, lib.moe_balance_loss, logits.data_ptr(), _DTYPES[logits.dtype], T, E, stride, topk_idx.data_ptr(),
             k, BALANCE_SCORES[score], _ptr(token_mask), _ptr(seq_offsets), S, coeff, loss.data_ptr(),
             counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return BalanceLoss(loss, counts, tokens, probs, k, score, coeff, token_mask, seq_offsets)
+    return BalanceLoss(loss, counts, tokens, probs, k, score, coeff, token_mask, seq_offsets, T)
 
 
 def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss: torch.Tensor,
@@ -965,6 +966,8 @@ def moe_balance_loss_backward(logits: torch.Tensor, fwd: BalanceLoss, grad_loss:
     S, E_fwd = counts.shape
     if E_fwd != E:
         raise ValueError(f"logits have {E} experts and the forward call had {E_fwd}")
+    if fwd.n_tokens is not None and fwd.n_tokens != T:
+        raise ValueError(f"logits have {T} tokens and the forward call had {fwd.n_tokens}")
     if mask is not None and mask.numel() != T:
         raise ValueError(f"logits have {T} tokens and the forward call's mask {mask.numel()}")
     _vector(grad_loss, torch.float32, "grad_loss", 1)

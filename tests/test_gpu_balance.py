@@ -280,3 +280,15 @@ def test_gradient_beside_and_over_the_logits(dtype):
     assert torch.equal(both, before)
     c.moe_balance_loss_backward(both[:T, :E], r, one, out=both[:T, E:])
     assert torch.equal(both[:T, E:], want) and torch.equal(both[:T, :E], before[:T, :E])
+
+
+def test_backward_takes_the_forward_calls_length():
+    require_cuda()
+    c = capi()
+    logits, idx = inputs(64, 16, 2, torch.float32)
+    r = c.moe_balance_loss(logits.cuda(), idx.cuda(), 0.1)
+    one = torch.ones(1, device="cuda")
+    assert r.n_tokens == 64
+    for other in (logits[:63], torch.cat([logits, logits]), logits[:0]):
+        with pytest.raises(ValueError, match="tokens"):
+            c.moe_balance_loss_backward(other.cuda(), r, one)

@@ -345,6 +345,18 @@ def test_sizes_past_32_bits_are_refused():
             call()
 
 
+def test_backward_refuses_logits_of_another_length():
+    """The counts hold for the forward call's tokens; without a mask nothing
+    else tells the two calls' lengths apart."""
+    c = capi()
+    t = ShapeOnly.of
+    fwd = c.BalanceLoss(t(1, dtype=torch.float32), t(1, 8, dtype=torch.int32), t(2, dtype=torch.int32),
+                        t(1, 8, dtype=torch.float32), 2, "sigmoid", 0.1, None, None, 6)
+    for T in (0, 5, 7):
+        with pytest.raises(ValueError, match=f"{T} tokens"):
+            c.moe_balance_loss_backward(t(T, 8, dtype=torch.float32), fwd, t(1, dtype=torch.float32))
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
     c = capi()
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
