@@ -21,6 +21,10 @@
  *     tokens [seq_offsets[s], seq_offsets[s+1]).  Tokens in no sequence are
  *     left out.  NULL: one sequence of all T tokens (S = 1).
  *   - choices outside [0, E) (a dropped slot) are not counted.
+ *   - the counts are those of the tokens that are not left out.  As the
+ *     expert_counts of a product on moe_route's rows, which hold every token,
+ *     they serve only without a mask and summed over sequences that together
+ *     hold every token.
  *   - an expert masked with a logit of -inf gets p = 0 and gradient 0; a token
  *     whose logits are all -inf has p = 0 throughout.
  * Sums are fp32 in a fixed order (fp64 where the partial sums join): the

@@ -840,7 +840,9 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, out_dtype: torch.dtype = torch.bfloat16, ou
     (sum_k a[m, k] b[n, k] + bias[n]), [M, N].  With ``expert_offsets`` (int32
     [E + 1], multiples of 128 as moe_route gives them) b holds E matrices of
     N rows and rows [offsets[e], offsets[e] + counts[e]) meet matrix e; the
-    other rows of ``out`` are left as they were (0 in a new one)."""
+    other rows of ``out`` are left as they were (0 in a new one).
+    ``expert_counts`` count every token that was routed: moe_balance_loss's
+    counts are fewer where it left tokens out."""
     if a.layout != "tiled":
         raise ValueError("a product takes tiled scales; quantise with layout='tiled'")
     if a.cols != b.cols:

@@ -121,3 +121,36 @@ def test_training_step_of_a_projection_behind_a_router():
     assert abs(float(loss[0]) - ref["loss"]) <= 1e-5 * ref["loss"]
     assert np.abs(dl - ref["dlogits"]).max() <= 4e-5 * np.abs(ref["dlogits"]).max()
     assert (dl[250:] == 0).all()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("offsets", [None, [0, 40, 40, 300], [10, 200, 290]])
+def test_routed_rows_beside_a_loss_that_leaves_tokens_out(masked, offsets):
+    """Every routed row is multiplied: with the loss's counts summed over the
+    sequences where it keeps every token, else without counts."""
+    require_cuda()
+    c = capi()
+    T, E, H, N, k = 300, 8, 256, 128, 2
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(T, H, generator=g).bfloat16()
+    w = (torch.randn(E, N, H, generator=g) * 0.05).bfloat16()
+    r = c.moe_route(x.cuda(), (torch.randn(E, H, generator=g) * 0.05).bfloat16().cuda(), torch.zeros(E, device="cuda"),
+                    k, 2.5)
+    mask = (torch.rand(T, generator=g) < 0.7).cuda() if masked else None
+    off = None if offsets is None else torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    b = c.moe_balance_loss(r["logits"], r["topk_idx"], 0.01, token_mask=mask, seq_offsets=off)
+    counts = b.counts.sum(0, dtype=torch.int32)
+    keeps_all = not masked and (offsets is None or offsets[0] == 0)
+    assert (int(counts.sum()) == T * k) == keeps_all
+    out = c.mxfp4_linear(x.cuda(), c.mxfp4_quantize(w.cuda()), perm=r["perm"], expert_offsets=r["expert_offsets"],
+                         expert_counts=counts if keeps_all else None, out_dtype=torch.float32)
+    xq, wq = mx(x.double().numpy()), mx(w.double().numpy().reshape(E * N, H)).reshape(E, N, H)
+    idx, got = r["topk_idx"].cpu().numpy(), np64(out[r["inv_perm"].long()])
+    for t in range(T):
+        for j in range(k):
+            m = wq[idx[t, j]]
+            # fp32 sums of H products, each addition truncated at most
+            assert (np.abs(got[t, j] - m @ xq[t]) <= (H + 2) * 2.0 ** -23 * (np.abs(m) @ np.abs(xq[t])) + 1e-30).all()
+    rest = torch.ones(out.shape[0], dtype=torch.bool)
+    rest[r["inv_perm"].reshape(-1).long().cpu()] = False
+    assert not out[rest.cuda()].any()
