@@ -101,6 +101,11 @@ NVFP4_API int nvfp4_test_router_splits(int T, int H, int* stages_per_split);
  * for sizes that mxfp4_matmul refuses. */
 NVFP4_API int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, int* pair, int* stages);
 
+/* Host arithmetic only: the CTAs of that product that an SM is to hold, with
+ * the dynamic shared memory and the tensor memory of each (nullable).  Returns
+ * -1 for sizes that mxfp4_matmul refuses. */
+NVFP4_API int nvfp4_test_mxfp4_residency(int M, int N, int K, int E, int* smem_bytes, int* tmem_columns);
+
 /* Host arithmetic only: the rows [row0[e], row0[e] + rows[e]) that expert e's
  * matrix meets in a grouped product of M rows, from `offsets` [E + 1] and
  * `counts` [E] (nullable), all in host memory.  Returns -1 for a NULL pointer

@@ -125,6 +125,7 @@ _declare("nvfp4_test_block_scale_div", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp
 _declare("nvfp4_test_router_splits", _i, _i, _i, ctypes.POINTER(ctypes.c_int))
 _declare("nvfp4_test_mxfp4_plan", _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
          ctypes.POINTER(ctypes.c_int))
+_declare("nvfp4_test_mxfp4_residency", _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int))
 _declare("nvfp4_test_mxfp4_segments", _i, _vp, _vp, _i, _i, _vp, _vp)
 _declare("nvfp4_test_mxfp4_fuses", _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int))
 
@@ -145,7 +146,7 @@ EXPORTS = ("nvfp4_last_error", "nvfp4_abi_version", "nvfp4_workspace_status",
            "nvfp4_test_e2m1", "nvfp4_test_e2m1_sweep", "nvfp4_test_e4m3", "nvfp4_test_sigmoid",
            "nvfp4_test_mma_peak", "nvfp4_test_wait_timeout", "nvfp4_test_block_scale_div",
            "nvfp4_test_router_splits", "nvfp4_test_mxfp4_plan", "nvfp4_test_mxfp4_segments",
-           "nvfp4_test_mxfp4_fuses")
+           "nvfp4_test_mxfp4_residency", "nvfp4_test_mxfp4_fuses")
 
 
 def _check(status: int):
@@ -1037,6 +1038,15 @@ def nvfp4_test_mxfp4_plan(M: int, N: int, K: int, E: int = 0):
     if nt < 0:
         raise ValueError(f"no MXFP4 product has M={M} N={N} K={K} E={E}")
     return nt, v[0].value, bool(v[1].value), v[2].value
+
+
+def nvfp4_test_mxfp4_residency(M: int, N: int, K: int, E: int = 0):
+    """(CTAs an SM is to hold, dynamic shared memory bytes, tensor memory columns of each) of an MXFP4 product."""
+    v = [ctypes.c_int(0) for _ in range(2)]
+    ctas = lib.nvfp4_test_mxfp4_residency(M, N, K, E, *(ctypes.byref(x) for x in v))
+    if ctas < 0:
+        raise ValueError(f"no MXFP4 product has M={M} N={N} K={K} E={E}")
+    return ctas, v[0].value, v[1].value
 
 
 def nvfp4_test_mxfp4_segments(offsets, counts, M: int):

@@ -100,11 +100,18 @@ struct MxGemmParams {
 // One stage: b codes, token codes, b scales, token scales.
 __host__ __device__ constexpr int mx_stage_bytes(int nt) { return kXWBytes + nt * kXRowBytes + 2 * kXSfBytes; }
 
-// Instruction descriptor: kind::mxf4, E2M1 x E2M1, UE8M0 scales, K-major
-// operands, M x N tile, the scales of byte pair `id` (0 or 2) of each word.
 // Fused: a stage holds b only; behind the stages, a's codes and scales of every K stage.
 constexpr int kXFuseStageBytes = kXWBytes + kXSfBytes;
 __host__ __device__ constexpr int mx_fused_a_bytes(int nt) { return nt * kXRowBytes + kXSfBytes; }
+// Columns of an accumulator, and tensor memory that a CTA allocates: its
+// accumulators and the scales of b and of the tokens behind them.
+__host__ __device__ constexpr int mx_acc_columns(int nt) { return nt > 32 ? nt : 32; }
+__host__ __device__ constexpr uint32_t mx_tmem_columns(int nt, int n_acc) {
+  const uint32_t need = (uint32_t)(n_acc * mx_acc_columns(nt)) + 4 * kXAtoms * 2;
+  return need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
+// Instruction descriptor: kind::mxf4, E2M1 x E2M1, UE8M0 scales, K-major
+// operands, M x N tile, the scales of byte pair `id` (0 or 2) of each word.
 NVDEV uint32_t idesc_mxf4(int M, int N, uint32_t id) {
   return (id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
          (id << 29);
@@ -321,10 +328,8 @@ __global__ void __launch_bounds__(kXThreads, 2)
   // that the next tile's MMAs run while one is drained; of two CTAs on an SM
   // one works while the other drains, and wide ones have half of tensor memory
   // each, room for one.
-  const int nt_pad = max(p.nt, 32);                          // columns of an accumulator
-  const int n_acc = p.n_acc;
-  const uint32_t need = (uint32_t)(n_acc * nt_pad) + 4 * kXAtoms * 2;
-  const uint32_t tcols = need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+  const int nt_pad = mx_acc_columns(p.nt), n_acc = p.n_acc;
+  const uint32_t tcols = mx_tmem_columns(p.nt, n_acc);
   // (FUSED: a's codes and scales lie behind the stages, for all of K)
   const int stage_bytes = FUSED ? kXFuseStageBytes : mx_stage_bytes(p.nt);
   const int x_bytes = FUSED ? 0 : p.nt * kXRowBytes;         // nt is a multiple of 16: whole 8-row swizzle groups
@@ -1392,6 +1397,15 @@ extern "C" int nvfp4_test_mxfp4_plan(int M, int N, int K, int E, int* splits, in
   if (pair) *pair = pl.pair ? 1 : 0;
   if (stages) *stages = pl.stages;
   return pl.nt;
+}
+
+extern "C" int nvfp4_test_mxfp4_residency(int M, int N, int K, int E, int* smem_bytes, int* tmem_columns) {
+  if (M < 1 || N < 1 || K < 1 || E < 0 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30) || E > kXMaxE) return -1;
+  const MxPlan pl = plan_mx_gemm(M, N, K, E, 148);
+  if (smem_bytes)
+    *smem_bytes = pl.stages * (pl.pair ? kPStageBytes : mx_stage_bytes(pl.nt)) + mx_segment_bytes(E) + 1024;
+  if (tmem_columns) *tmem_columns = pl.pair ? 512 : (int)mx_tmem_columns(pl.nt, pl.n_acc);
+  return pl.ctas_per_sm;
 }
 
 extern "C" int nvfp4_test_mxfp4_fuses(int M, int N, int K, int dtype, int wide, int* stages, int* ctas_per_sm) {

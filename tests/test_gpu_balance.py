@@ -292,3 +292,25 @@ def test_backward_takes_the_forward_calls_length():
     for other in (logits[:63], torch.cat([logits, logits]), logits[:0]):
         with pytest.raises(ValueError, match="tokens"):
             c.moe_balance_loss_backward(other.cuda(), r, one)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,off", [(200, [0, 90, 200]), (200, [0, 0, 200]), (200, [0, 200, 200]), (200, [0, 0, 0]),
+                                   (200, [7, 7, 150]), (200, [200, 200, 200]), (1, [0, 0, 1]), (0, [0, 0, 0]),
+                                   (200, [5, 190]), (200, [200, 200]), (682, [0, 300, 682])])
+def test_one_kernel_takes_one_or_two_sequences(T, off, score):
+    """Up to 16,384 logits in at most two sequences are one kernel's work:
+    empty sequences, and masks that empty one of the two or both."""
+    require_cuda()
+    c = capi()
+    logits, idx = inputs(T, 24, 3, torch.float32)
+    masks = [None]
+    if T:
+        for first, last in ((0, T), (off[0], off[1]), (off[-2], off[-1]), (T // 2, T // 2 + 1)):
+            m = torch.ones(T, dtype=torch.bool)
+            m[first:last] = False
+            masks.append(m)
+    for m in masks:
+        r, d = check(c, logits, idx, 0.5, score, mask=m, off=off)
+        if int(r.tokens[-1]) == 0:
+            assert float(r.loss) == 0.0 and not r.probs.any() and not r.counts.any() and not d.any()

@@ -196,6 +196,38 @@ def test_product_plans():
             plan(*bad)
 
 
+def test_products_that_share_an_sm_fit_it():
+    """Host arithmetic: the CTAs that a plan puts on an SM fit its shared
+    memory (228 KiB, 1 KiB of it taken by each CTA, and 256 bytes of static
+    variables) and its 512 columns of tensor memory, whose allocation would
+    otherwise wait for the other CTA's end."""
+    c = capi()
+    seen = set()
+    sizes = (1, 16, 17, 32, 33, 48, 64, 65, 128, 129, 256, 1000, 3000, 4096, 20000, 100000)
+    for M in sizes:
+        for N in (1, 128, 384, 1024, 6144, 12288, 18944, 100096):
+            for K in (1, 256, 300, 2048, 6144, 20000):
+                for E in (0, 1, 8, 80, 480, 481, 1024):
+                    if E and N % 128:
+                        continue
+                    nt, splits, pair, stages = c.nvfp4_test_mxfp4_plan(M, N, K, E)
+                    ctas, smem, columns = c.nvfp4_test_mxfp4_residency(M, N, K, E)
+                    seen.add((ctas, columns, splits > 1, pair))
+                    assert ctas in (1, 2) and columns in (64, 128, 256, 512)
+                    assert smem <= 228 * 1024 // ctas - 1024 - 256
+                    assert ctas * columns <= 512 and (not pair or columns == 512)
+                    # an accumulator's columns and two 4-column scale atoms of either operand
+                    assert pair or columns >= max(nt, 32) + 16
+                    # what a few tokens are planned for
+                    assert pair or nt > 64 or E or ctas == 2
+    assert {(2, 128, True, False), (2, 256, False, False), (1, 512, False, False), (1, 512, False, True)} <= seen
+    for M in (1, 16):                                    # fused: one accumulator of 32 columns and the scales
+        ctas = c.nvfp4_test_mxfp4_fuses(M, 1024, 6144, torch.bfloat16)[1]
+        assert ctas * 64 <= 512
+    with pytest.raises(ValueError):
+        c.nvfp4_test_mxfp4_residency(0, 1, 1)
+
+
 def test_segments_of_grouped_products():
     """Host arithmetic shared with the kernels: whatever the number of rows,
     each expert has the clamped rows of its own segment and no others."""
