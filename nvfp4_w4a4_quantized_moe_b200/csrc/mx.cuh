@@ -45,7 +45,6 @@ struct Bf16 {
   NVDEV static float hi(uint32_t w) { return bf16_hi(w); }
   NVDEV static uint32_t pack(float a, float b) { return pack_bf16x2(a, b); }
   NVDEV static uint16_t one(float a) { return (uint16_t)pack_bf16x2(a, 0.0f); }
-  NVDEV static float from(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
   NVDEV static uint32_t mag(uint32_t h) { return h << 16; }          // |h| as fp32 bits
 };
 struct F16 {
@@ -58,18 +57,17 @@ struct F16 {
     return r;
   }
   NVDEV static uint16_t one(float a) { return __half_as_ushort(__float2half_rn(a)); }
-  NVDEV static float from(uint16_t h) { return __half2float(__ushort_as_half(h)); }
-  NVDEV static uint32_t mag(uint32_t h) { return __float_as_uint(from((uint16_t)h)) & 0x7FFFFFFFu; }
+  NVDEV static uint32_t mag(uint32_t h) {
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h))) & 0x7FFFFFFFu;
+  }
 };
 struct F32 {
   static constexpr int size = 4;
 };
 
-// |v| as an integer that orders like the magnitude, with every infinity and
-// NaN above every finite value.
-NVDEV uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-// E8M0 byte of a block from the mag_bits of its largest element: the exponent
+// E8M0 byte of a block from its largest magnitude, as the bits of fp32 without
+// the sign (they order like the magnitudes, with every infinity and NaN above
+// every finite value): the exponent
 // field less 2 (floor(log2 a) - 2 + 127), 0 where that would be below 2^-127
 // (subnormal maxima included), 255 for a block with a NaN or an infinity.
 NVDEV uint32_t mx_scale(uint32_t amax_bits) {
@@ -120,7 +118,9 @@ inline int row_access_bytes(const void* p, long long stride_bytes, int elem) {
   return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : a % 8 == 0 ? 8 : a % 4 == 0 ? 4 : elem;
 }
 
-// 32 consecutive bytes as eight words, in accesses of VB bytes.
+// 32 consecutive bytes as eight words, in loads of VB bytes (32, 16 or 8) and
+// stores of VB bytes (32 or 16); narrower rows are read shifted and written
+// through shared memory.
 template <int VB>
 NVDEV void load_words8(const void* p, uint32_t* w) {
   if constexpr (VB == 32) {
@@ -133,15 +133,13 @@ NVDEV void load_words8(const void* p, uint32_t* w) {
       const uint4 v = __ldg(static_cast<const uint4*>(p) + i);
       w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
-  } else if constexpr (VB == 8) {
+  } else {
+    static_assert(VB == 8, "width of a load");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint2 v = __ldg(static_cast<const uint2*>(p) + i);
       w[2 * i] = v.x; w[2 * i + 1] = v.y;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __ldg(static_cast<const uint32_t*>(p) + i);
   }
 }
 template <int VB>
@@ -150,16 +148,11 @@ NVDEV void store_words8(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-  } else if constexpr (VB == 16) {
+  } else {
+    static_assert(VB == 16, "width of a store");
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  } else if constexpr (VB == 8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) static_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) static_cast<uint32_t*>(p)[i] = w[i];
   }
 }
 
@@ -216,7 +209,7 @@ NVDEV void load_share(const uint8_t* row, int c, int n, const uint8_t* lo, const
   }
 }
 
-// mag_bits of the largest element of the block that these lanes share
+// fp32 bits of the largest magnitude of the block that these lanes share
 // (magnitudes compare as integers; packed pairs for 16-bit types).
 template <typename T>
 NVDEV uint32_t share_amax(const uint32_t* w) {

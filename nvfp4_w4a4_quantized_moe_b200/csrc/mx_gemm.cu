@@ -62,7 +62,7 @@ constexpr int kXThreads = 320;
 constexpr int kXEpiWarps = 8;
 constexpr int kXMaxStages = 8;
 constexpr int kXMaxE = 1024;
-constexpr int kXMaxSplits = 8;                   // the largest portable cluster
+constexpr int kXMaxSplits = 4;                   // CTAs of a cluster that share K, at most (plan_mx_gemm)
 // Dynamic shared memory of a CTA that has an SM to itself, and of one of two
 // on an SM (228 KiB less 1 KiB a CTA; the static part is below 256 bytes).
 constexpr int kXMaxSmem = 227 * 1024 - 256;
@@ -1053,11 +1053,13 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   }
   // a single token tile is no wider than its tokens
   pl.nt = E == 0 && M <= kXNT ? (M + 15) / 16 * 16 : kXNT;
-  // Few tokens: two CTAs on an SM, and K split over a cluster while there are
-  // SMs for it.  Measured at N = K = 6144 (48 tiles) and one token, splits of
-  // 1, 2, 3, 4, 6, 8: 10.8, 7.8, 7.6, 7.0, 11.4, 11.2 us; at N = 1024 (8
-  // tiles) 10.2, 6.9, 5.8, 5.1, 4.7, 4.4; at N = 5001, K = 2010 (40 tiles) 6.0,
-  // 5.7, 5.5, 6.6, 6.7, 11.0; wider tiles, at one CTA an SM (128 tokens, 48
+  // Few tokens: two CTAs on an SM, and K split over a cluster while there is
+  // an SM for each of its CTAs.  Measured at N = K = 6144 (48 tiles) and one
+  // token, splits of 1, 2, 3, 4, 6, 8: 10.8, 7.8, 7.6, 7.0, 11.4, 11.2 us; at N
+  // = 1024 (8 tiles) 10.2, 6.9, 5.8, 5.1, 4.7, 4.4; at N = 5001, K = 2010 (40
+  // tiles) 6.0, 5.7, 5.5, 6.6, 6.7, 11.0.  One rule for all of them: it takes 3
+  // splits at 48 tiles and at 40, where 4 gain 0.6 us and lose 1.1, and stops at
+  // 4, where 8 tiles would still gain 0.7 from 8.  Wider tiles, at one CTA an SM (128 tokens, 48
   // tiles): 12.2, 11.2, then 17 and more, as clusters of three and more no
   // longer fit at once; with 16 tiles (100 x 2048 x 6144) 11.6, 9.3, 7.8, 7.2,
   // 7.5, 13.4.  Joining 128 columns costs 2 us: at 8 stages (128 x 4096 x 2048)
@@ -1069,7 +1071,7 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
   pl.stages = std::min(kXMaxStages, ((pl.ctas_per_sm == 2 ? kXSmemPair : kXMaxSmem) - 1024 - table) / stage);
   if (E == 0) {
     const long long all = (long long)n_wt * ((M + pl.nt - 1) / pl.nt);
-    const long long most = pl.nt <= 64 ? 4 : kt < 12 ? 1 : all * 4 <= sms / 2 ? 4 : 2;
+    const long long most = pl.nt <= 64 ? kXMaxSplits : kt < 12 ? 1 : all * 4 <= sms / 2 ? kXMaxSplits : 2;
     pl.splits = (int)std::max(1ll, std::min({most, sms / all, (long long)(kt + 1) / 2}));
   }
   return pl;
