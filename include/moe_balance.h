@@ -14,9 +14,9 @@
  *   dloss/dlogit[t][e] = coeff / (S' n_s) p_t[e] (f[s][e] - sum_j f[s][j] p_t[j]) * d
  * with d = 1 for softmax and sigma(-logit) for sigmoid.
  *
- *   - token_mask (uint8 [T], nullable): tokens with 0 are left out; their
- *     logits are not looked at (they may hold anything) and their gradient is
- *     0.
+ *   - token_mask (uint8 [T], nullable): tokens with 0 are left out: their
+ *     logits and choices are read, and dropped whatever they hold (NaN and
+ *     infinities too); their gradient is 0.
  *   - seq_offsets (int32 [S+1], nullable, non-decreasing): sequence s is the
  *     tokens [seq_offsets[s], seq_offsets[s+1]).  Tokens in no sequence are
  *     left out.  NULL: one sequence of all T tokens (S = 1).

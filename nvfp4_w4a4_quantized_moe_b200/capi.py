@@ -925,7 +925,8 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, coeff: float,
     fp16, any row stride) and choices topk_idx [T, k] (int32, as moe_route
     gives them).  ``token_mask`` (bool or uint8 [T]): tokens to count.
     ``seq_offsets`` (int32 [S + 1]): the loss per sequence, averaged over the
-    sequences that have tokens."""
+    sequences that have tokens.  The loss is no node of an autograd graph: its
+    gradient is moe_balance_loss_backward's."""
     T, E, stride = _matrix(logits, "logits")
     idx_shape = _cuda(topk_idx, torch.int32, "topk_idx").shape
     if len(idx_shape) != 2 or idx_shape[0] != T:

@@ -16,14 +16,16 @@
 // Bound: HBM (logits in; gradient out) behind a dozen instructions an element,
 // one exponential (softmax) or one exponential and one reciprocal (sigmoid)
 // among them; below some ten thousand tokens the chain of loads, joins and
-// launches.  Measured on one B200 (128 experts, top-8, softmax, us forward and
-// backward, logits from HBM):
-//                                        fp32          bf16
-//   262,144 tokens, 33 sequences, mask   38.9, 50.7    36.4, 36.5
-//   65,531 tokens, 17 sequences, mask    20.0, 15.7    18.9, 13.1
-//   65,531 tokens, one sequence          15.9, 15.2    15.2, 11.7
-//   4,096 tokens, one sequence            8.6,  3.1     8.4,  3.1
-//   16 tokens of 80 experts               3.3,  2.5     3.3,  2.5
+// launches.  Measured on one B200 (top-8, us forward and backward, logits from
+// HBM):
+//                                               softmax                 sigmoid
+//                                          fp32        bf16        fp32        bf16
+//   262,144 x 128, 33 sequences, mask   38.7, 50.3  36.8, 36.4  42.5, 53.5  42.7, 43.7
+//   65,531 x 128, 17 sequences, mask    21.5, 15.5  19.2, 12.5  21.5, 16.5  20.3, 14.4
+//   65,531 x 128, one sequence          16.5, 14.6  15.7, 10.9  17.4, 15.4  16.9, 13.0
+//   262,144 x 80, one sequence          32.7, 38.4  30.9, 30.0  35.3, 42.1  34.5, 35.4
+//   8,192 x 80, one sequence             8.9,  3.7   9.3,  3.8   9.2,  3.9   9.4,  4.2
+//   16 x 80                              3.4,  2.6   3.4,  2.6   3.5,  2.7   3.5,  2.6
 // What brought it there: four logits a lane and row (five shuffles for each
 // maximum and sum), a reciprocal a logit for softmax too and the choices counted
 // before the rows, 57 and 31 us at 65,536 tokens fp32; sixteen a lane 23 and 17
@@ -635,7 +637,9 @@ static inline int balance_chunk(int T, int E) {
 // Few logits: one block does the whole forward, one launch instead of two.
 // Measured, one block against two kernels (us): 16 x 80 3.5 and 7.8, 64 x 80
 // 4.3 and 7.9, 128 x 128 6.2 and 8.5, 192 x 128 7.7 and 8.4, 256 x 128 9.1 and
-// 8.4, 512 x 128 14.7 and 8.1.  It walks its sequences one after the other, 2.3
+// 8.4, 512 x 128 14.7 and 8.1: the limit of 16,384 logits lies below the
+// crossing, which was not sought closer than between 24,576 and 32,768.  The
+// block walks its sequences one after the other, 2.3
 // us each (128 x 128 in 20: 50 and 27, in 60: 144 and 47), hence at most two.
 static inline bool balance_one_block(int T, int E, int S) { return (long long)T * E <= kBalOneBlock && S <= 2; }
 
@@ -680,6 +684,13 @@ static nvfp4_status check_balance(const char* name, const void* logits, int dtyp
 }
 
 // Calls f(type tag, vector loads allowed, quads of logits per lane, score).
+// Each number of quads has its kernel: with four in place of one, two and three
+// (whose further logits are -inf) 65,536 tokens, fp32 softmax and bf16 sigmoid,
+// took, us forward and backward, own kernel against four quads:
+//   4 experts (1)    8.5, 2.5 and 10.9, 2.8     8.4, 2.6 and 11.5, 3.9
+//   8 experts (2)    8.8, 3.0 and 10.7, 3.2     8.6, 2.9 and 11.1, 4.1
+//   40 experts (3)   12.6, 6.7 and 13.8, 7.4    12.9, 7.3 and 13.9, 8.7
+//   80 experts (3)   15.4, 10.3 and 16.6, 11.0  15.1, 11.2 and 17.4, 13.4
 template <typename F>
 static nvfp4_status with_balance(int dtype, bool vec, int E, int score, F&& f) {
   const int quads = ((E + 3) / 4 + balance_lanes(E) - 1) / balance_lanes(E);

@@ -31,7 +31,7 @@
 // bf16 outputs, in a stream of calls:
 //   8192 x 4096 x 6144   72 us, 5.7 PFLOP/s (0.86 of four times the measured
 //                        bf16 rate)
-//   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 8.6
+//   1024 x 4096 x 6144   16 us; 256 x 6144 x 6144 13 us; 64 x 6144 x 6144 9.7
 //   16 x 6144 x 6144     8.1 us, 2.4 TB/s; 1 x 6144 x 6144 7.5 us (b in L2: 6.8, 6.5)
 //   1 x 6144 x 6144 with x quantised in the same kernel 7.9 us (two kernels 9.5)
 //   16 tokens, top-8 of 80 experts, 4096 x 6144: 140 us, 97 % of the copy rate
@@ -1080,9 +1080,10 @@ static MxPlan plan_mx_gemm(int M, int N, int K, int E, int sms) {
 // The plan of a product that quantises its own tokens, from the plan of one
 // that does not; false where there is none or it would be slower.  It takes a
 // single token tile, a tile a CTA, and a's share of K beside three stages (four
-// where K is split) at least.  Every CTA converts the tokens for itself, which costs 0.4 us a pass
-// (32 units of 128 elements, 16 of fp32; more where rows are not 16-byte
-// aligned) where the quantiser's launch costs 2 on the GPU and 2.5 on the host.
+// where K is split) at least.  Every CTA converts the tokens for itself, which
+// costs 0.4 us a pass (32 units of 128 elements, 16 of fp32; more where rows are
+// not 16-byte aligned) where the quantiser's launch costs 2 on the GPU and 2.5
+// on the host.
 // Measured, tokens: us fused, us with the quantiser's kernel
 //   bf16  1024 x 6144 (6 stages a CTA)    1: 5.4, 7.2   8: 5.7, 7.4  16: 7.0, 7.6
 //         6144 x 6144 (8 stages)          1: 7.9, 9.5   8: 8.8, 9.9  12: 10.1, 10.0
