@@ -314,3 +314,33 @@ def test_one_kernel_takes_one_or_two_sequences(T, off, score):
         r, d = check(c, logits, idx, 0.5, score, mask=m, off=off)
         if int(r.tokens[-1]) == 0:
             assert float(r.loss) == 0.0 and not r.probs.any() and not r.counts.any() and not d.any()
+
+
+def test_offsets_past_32_bits():
+    """Logits and gradient of more than 2^32 elements: the last tokens, a
+    sequence of their own, come out as they do by themselves."""
+    require_cuda()
+    c = capi()
+    T, E, n = 2 ** 25 + 300, 128, 300                          # 8.6 GB of bf16 each
+    tail, idx = inputs(n, E, 2, torch.bfloat16)
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    logits[-n:] = tail.cuda()
+    choice = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    choice[-n:] = idx.cuda()
+    off = torch.tensor([0, T - n, T], dtype=torch.int32, device="cuda")
+    g = torch.full((1,), 2.0 ** 10, device="cuda")
+    r = c.moe_balance_loss(logits, choice, 1.0, "softmax", seq_offsets=off)
+    d = c.moe_balance_loss_backward(logits, r, g)
+    alone, d_alone = check(c, tail, idx, 1.0, "softmax", grad=2.0 ** 9)      # one sequence of one, not of two
+    assert r.tokens.tolist() == [T - n, n, 2] and int(r.counts[0, 0]) == 2 * (T - n)
+    assert torch.equal(r.counts[1:], alone.counts) and torch.equal(d[-n:], d_alone)
+    # other pieces, so another order: 300 additions at most, each off by 2^-24
+    assert (r.probs[1] - alone.probs[0]).abs().max() <= 300 * 2.0 ** -24 * alone.probs.max()
+    # equal shares of 2^-7 add exactly; the mean is one division of two rounded numbers
+    assert (r.probs[0] * 128 - 1).abs().max() <= 3 * 2.0 ** -24
+    # f is 128 for the one expert that all choose: p (f - <f, p>) = (128 - 1) / 128 there, -1 / 128 elsewhere
+    want = torch.full((E,), -1.0 / 128, dtype=torch.float64)
+    want[0] = 127.0 / 128
+    want *= 2.0 ** 10 / (2 * (T - n))
+    for t in (0, 1, T // 2, T - n - 1):
+        assert ((d[t].double().cpu() - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -22) * want.abs()).all()
