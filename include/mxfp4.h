@@ -31,8 +31,8 @@
  * Conventions are those of nvfp4_moe.h (device memory of the caller, nothing
  * allocated, work queued on `stream`, checks on the host before anything is
  * queued).  A workspace serves one call at a time: calls or captured graphs
- * that share one run one after the other.  Sizes of zero rows are legal and
- * queue nothing.
+ * that share one run one after the other.  Outputs share no memory with inputs
+ * but where a call allows it.  Sizes of zero rows are legal and queue nothing.
  */
 #ifndef NVFP4_MOE_MXFP4_H
 #define NVFP4_MOE_MXFP4_H
